@@ -67,8 +67,10 @@ typedef enum {
     RA_ERR_WORKSPACE = 3,     /* ws null, misaligned or smaller than required      */
     RA_ERR_CUDA = 4,          /* a CUDA runtime call or kernel launch failed       */
     RA_ERR_TIMEOUT = 5,       /* a device-side wait expired (see device_status)    */
-    RA_ERR_RANGE = 6          /* an input exceeds the fp16 range of the bf16 path's
+    RA_ERR_RANGE = 6,         /* an input exceeds the fp16 range of the bf16 path's
                                  score operands (see device_status)                */
+    RA_ERR_CACHE = 7          /* a page, length or offset of a batch lies outside the
+                                 cache or the batch (see device_status)            */
 } ra_status;
 
 typedef enum { RA_F32 = 0, RA_BF16 = 1 } ra_dtype;
@@ -207,11 +209,153 @@ typedef struct {
 ra_status rope_attn_alpha_adam(const ra_adam* opt, int64_t count, float* alpha,
                                const float* dalpha, float* m1, float* m2, void* stream);
 
+/* ---- rotary positions outside the attention step --------------------------------
+ * The rotation by itself, for positions that are not 0..n-1 and for the layouts in use:
+ *   y = A R(p theta_hat) x on the first rot_dim channels of every head (the rest is copied),
+ *   theta_hat_m = e^alpha_m s_m(base^(-2m / rot_dim)), m = 0..rot_dim/2 - 1
+ * ("LeRoPE", Declaracao do Problema and Mecanismo Central).  Band m is the channel pair
+ * (2m, 2m + 1) in the interleaved layout, (m, m + rot_dim/2) in the half layout.  s is the
+ * scaling for contexts longer than the trained one (A the amplitude of cos and sin):
+ *   RA_SCALE_NONE    s(t) = t
+ *   RA_SCALE_LINEAR  s(t) = t / factor
+ *   RA_SCALE_PARTS   s(t) = (1 - g) t / factor + g t, g = clamp((orig_len t / 2 pi - slow) /
+ *                    (fast - slow), 0, 1): bands that turn less than `slow` times over
+ *                    orig_len positions are interpolated, those above `fast` times kept.
+ * fixed_bands as in ra_problem (theta_hat_m = 0 for the slowest ones). */
+typedef enum { RA_INTERLEAVED = 0, RA_HALF = 1 } ra_layout;
+typedef enum { RA_SCALE_NONE = 0, RA_SCALE_LINEAR = 1, RA_SCALE_PARTS = 2 } ra_scaling;
+
+typedef struct {
+    int64_t d, rot_dim;       /* channels of a head (even, 2..256); rotated ones (even, 2..d) */
+    double base;              /* RoPE base > 0                                               */
+    double factor, orig_len;  /* > 0 where the scaling uses them                             */
+    double slow, fast;        /* slow < fast, RA_SCALE_PARTS                                 */
+    double amplitude;         /* A (1: a pure rotation)                                      */
+    int32_t layout, scaling;  /* ra_layout, ra_scaling                                       */
+    int32_t fixed_bands;      /* 0..rot_dim/2                                                */
+    int32_t reserved;         /* must be 0                                                   */
+} ra_rotary;
+
+/* Rows of heads: element (b, h, i, c) lies at ptr[b stride_b + h stride_h + i stride_n + c]
+ * (strides in elements, >= 0; the channels of a head are contiguous).  A written tensor's
+ * rows must not overlap (RA_ERR_INVALID_ARG).  16-byte aligned pointers and strides and whole
+ * 16-byte vectors per rotated half move as vectors; anything else element by element. */
+typedef struct {
+    void* ptr;
+    int64_t H, stride_b, stride_h, stride_n;
+} ra_rows;
+
+/* freqs [rot_dim/2] fp64 = theta_hat.  alpha [rot_dim/2] fp32, or NULL for zeros.  The caller
+ * keeps freqs; the calls below take it (one call per change of alpha). */
+ra_status rope_attn_rotary_freqs(const ra_rotary* r, const float* alpha, double* freqs,
+                                 void* stream);
+
+/* q_out, k_out = the rotated q, k: B batches of n tokens, dtype a ra_dtype.  pos [B, n] int32
+ * (any sign), or NULL for i at token i.  k and k_out may both be NULL.  An output may be its
+ * input (same pointer and strides), not overlap it otherwise.  The angle is formed and reduced
+ * in fp64, cos and sin rounded to fp32, the turn computed in fp32 and rounded once to the
+ * dtype.  B n <= 2^30. */
+ra_status rope_attn_rotary(const ra_rotary* r, int64_t B, int64_t n, int32_t dtype,
+                           const double* freqs, const int32_t* pos, const ra_rows* q,
+                           const ra_rows* q_out, const ra_rows* k, const ra_rows* k_out,
+                           void* stream);
+
+/* Gradients: dq, dk from dq_rot, dk_rot (those of the rotated tensors), and dalpha
+ * [rot_dim/2] fp32 summed over q and k, every batch, head and token (q, k: the forward's
+ * inputs; dalpha_m = theta_hat_m sum p <dx_m, J x_m> in fp64, fixed order: deterministic).
+ * dalpha NULL: frozen frequencies; q, k and ws are then not read.  The k tensors may all be
+ * NULL.  dq may be dq_rot (same strides), not q.  ws: rope_attn_rotary_workspace_bytes(r)
+ * bytes, 256-byte aligned, needed with dalpha only. */
+size_t rope_attn_rotary_workspace_bytes(const ra_rotary* r);
+ra_status rope_attn_rotary_bwd(const ra_rotary* r, int64_t B, int64_t n, int32_t dtype,
+                               const double* freqs, const int32_t* pos, const ra_rows* dq_rot,
+                               const ra_rows* dq, const ra_rows* dk_rot, const ra_rows* dk,
+                               const ra_rows* q, const ra_rows* k, float* dalpha, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* ---- a paged cache of keys and values held in 4 bits ---------------------------------
+ * For serving: the keys are rotated as they enter the cache, so attention over it needs no
+ * positions.  A page holds page_size tokens (a multiple of 16) of every kv head.  The cache is
+ * [pages][Hkv][page_size / 16] blocks of 16 tokens, each block
+ *   [K codes 16 x d/2 | K pairs 16 x d/64 x 4 | V codes 16 x d/2 | V pairs 16 x d/64 x 4] bytes
+ * (rope_attn_cache_block_bytes(d): 1152 at d = 64, 2304 at d = 128; 4.5 bits per value).
+ * Codes are 4 bits in channel order, even channel in the low nibble; a pair is (step, lo) in
+ * fp16 for 64 channels.  A code stands for lo + step * code.  lo is the smallest of the 64
+ * values, step (largest - lo) / 15, each rounded to fp16 (computed in fp32); the code is
+ * (x - lo) * (1 / step) rounded to the nearest whole number (ties to even), within 0..15.
+ * Values beyond +-RA_CACHE_LIMIT are clamped and NaN becomes 0, reported as RA_ERR_RANGE.
+ *
+ * A batch is B sequences with T rows of tokens packed one after the other: sequence b has the
+ * rows indptr[b] .. indptr[b+1] - 1 (indptr [B + 1] int32, rising, indptr[B] <= T; rows from
+ * indptr[B] on belong to nobody and are neither read nor written), which are the LAST ones of
+ * its kv_len[b] cached tokens (int32): row indptr[b] + i is position kv_len[b] - qlen + i.
+ * Position p of sequence b lies in page table[b][p / page_size] (table [B][max_pages] int32).
+ * The device checks what it reads of these: a falling indptr or one outside 0..T, a sequence
+ * of more than max_q tokens, kv_len outside 0..max_pages page_size (append and read: or below
+ * the sequence's own tokens), or a used page outside 0..pages-1 is recorded as RA_ERR_CACHE
+ * (info: kernel id, what (RA_CACHE_BAD_*), sequence) and never followed: a bad sequence is
+ * skipped (its outputs are not valid), the tokens of a bad page are neither written nor read
+ * (attention sees them as masked, reads give zeros).  Sequences may share pages to read; two sequences that append to one slot in
+ * one call leave it undefined.
+ *
+ * ws (all calls): rope_attn_cache_workspace_bytes(p) bytes, 256-byte aligned.  Its first 64
+ * bytes are the error word: zero them once; the calls never clear it (the first error stays
+ * until rope_attn_device_status reads and clears it), so that one check covers a whole decode
+ * step of many calls.  The rest holds nothing between calls.  Calls that overlap on the GPU
+ * need a workspace each. */
+typedef struct {
+    int64_t B, T;             /* sequences 1..65536; rows of q, k, v, o, lse, 0 <= T <= 2^30 */
+    int64_t Hq, Hkv;          /* Hq a multiple of Hkv; Hkv <= 1024, Hq <= 4096,
+                                 T Hq d <= 2^38                                             */
+    int64_t d;                /* 64 or 128                                                   */
+    int64_t pages, page_size; /* 1..2^30; multiple of 16, 16..4096                           */
+    int64_t max_pages;        /* width of table; max_pages page_size <= 2^30                 */
+    int64_t max_q;            /* most tokens of one sequence in a call; 0: T                 */
+    int64_t window;           /* causal only: keys seen, the row's own included; 0: all      */
+    double scale;             /* of q k^T; 0: 1 / sqrt(d)                                    */
+    int32_t dtype;            /* ra_dtype of q, k, v, o                                      */
+    int32_t causal;           /* 1: row at position p sees keys <= p; 0: all kv_len keys     */
+} ra_cache;
+
+#define RA_CACHE_LIMIT 60000.0f
+enum { RA_CACHE_BAD_INDPTR = 1, RA_CACHE_BAD_LENGTH = 2, RA_CACHE_BAD_PAGE = 3 };
+
+size_t rope_attn_cache_block_bytes(int64_t d);            /* 0: unsupported d        */
+size_t rope_attn_cache_bytes(const ra_cache* p);          /* of the whole cache      */
+size_t rope_attn_cache_workspace_bytes(const ra_cache* p);
+
+/* Appends the batch's tokens: k (rotated by r at its position, then quantised) and v into the
+ * cache, and, where q is given, q_out = q rotated at the same positions (q_out may be q).
+ * k, v [T, Hkv, d], q, q_out [T, Hq, d]: stride_n and stride_h of the rows (stride_b unused).
+ * r->d must be p->d.  kv_len counts the appended tokens already. */
+ra_status rope_attn_cache_append(const ra_cache* p, void* cache, const int32_t* table,
+                                 const int32_t* indptr, const int32_t* kv_len,
+                                 const ra_rotary* r, const double* freqs, const ra_rows* k,
+                                 const ra_rows* v, const ra_rows* q, const ra_rows* q_out,
+                                 void* ws, size_t ws_bytes, void* stream);
+
+/* The cached keys (as rotated) and values of the batch's tokens, as the values that they stand
+ * for: k, v [T, Hkv, d] rows in the dtype; either may be NULL. */
+ra_status rope_attn_cache_read(const ra_cache* p, const void* cache, const int32_t* table,
+                               const int32_t* indptr, const int32_t* kv_len, const ra_rows* k,
+                               const ra_rows* v, void* ws, size_t ws_bytes, void* stream);
+
+/* o = softmax(scale q K^T + mask) V over the cache, lse = log-sum-exp of each row (natural
+ * log).  q [T, Hq, d] rows (already rotated), o dense [T, Hq, d], lse dense fp32 [T, Hq];
+ * q head h reads kv head h / (Hq / Hkv).  A row that sees no key gives o = 0, lse = -inf.
+ * bf16: tensor cores (mma.sync for a few rows, tcgen05 for chunks); the codes enter the score
+ * products exactly, V as fp16 lo + step * code and P as fp16, everything summed in fp32.
+ * fp32: CUDA cores, fp32 throughout.  Deterministic: no atomics, fixed order. */
+ra_status rope_attn_cache_attn(const ra_cache* p, const void* cache, const int32_t* table,
+                               const int32_t* indptr, const int32_t* kv_len, const ra_rows* q,
+                               void* o, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, reads and clears the device error word in ws.
  * Returns RA_OK; RA_ERR_TIMEOUT if a kernel gave up on a wait during the most recent
  * call on ws (kernel id / wait site / block id are written to info[0..2] when info is
- * non-null); or RA_ERR_RANGE if a rotated query or key entry exceeded the fp16 range
- * of the bf16 path's score operands. */
+ * non-null); RA_ERR_RANGE if a rotated query or key entry exceeded the fp16 range
+ * of the bf16 path's score operands (or an appended value RA_CACHE_LIMIT); or RA_ERR_CACHE
+ * from a cache call (info: kernel id, RA_CACHE_BAD_*, sequence). */
 ra_status rope_attn_device_status(void* ws, size_t ws_bytes, void* stream, int32_t info[3]);
 
 /* Static text for a status code. */

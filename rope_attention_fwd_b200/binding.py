@@ -16,7 +16,9 @@ LIB_PATH = os.path.join(_PKG, "librope_attn.so")
 RA_F32, RA_BF16 = 0, 1
 _DTYPE = {torch.float32: RA_F32, torch.bfloat16: RA_BF16}
 STATUS = {0: "RA_OK", 1: "RA_ERR_INVALID_ARG", 2: "RA_ERR_UNSUPPORTED", 3: "RA_ERR_WORKSPACE",
-          4: "RA_ERR_CUDA", 5: "RA_ERR_TIMEOUT", 6: "RA_ERR_RANGE"}
+          4: "RA_ERR_CUDA", 5: "RA_ERR_TIMEOUT", 6: "RA_ERR_RANGE", 7: "RA_ERR_CACHE"}
+LAYOUTS = {"interleaved": 0, "half": 1}
+SCALINGS = {"none": 0, "linear": 1, "parts": 2}
 
 
 class RaProblem(ctypes.Structure):
@@ -29,6 +31,26 @@ class RaProblem(ctypes.Structure):
 class RaAdam(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
                 ("eps", ctypes.c_float), ("clip_norm", ctypes.c_float), ("step", ctypes.c_int32)]
+
+
+class RaRotary(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int64), ("rot_dim", ctypes.c_int64), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("orig_len", ctypes.c_double),
+                ("slow", ctypes.c_double), ("fast", ctypes.c_double),
+                ("amplitude", ctypes.c_double), ("layout", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("fixed_bands", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class RaRows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("H", ctypes.c_int64), ("stride_b", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64), ("stride_n", ctypes.c_int64)]
+
+
+class RaCache(ctypes.Structure):
+    _fields_ = [(x, ctypes.c_int64) for x in ("B", "T", "Hq", "Hkv", "d", "pages", "page_size",
+                                              "max_pages", "max_q", "window")] + \
+               [("scale", ctypes.c_double), ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32)]
 
 
 class RopeAttnError(RuntimeError):
@@ -82,6 +104,29 @@ def lib():
         L.rope_attn_device_status.restype = ctypes.c_int
         L.rope_attn_status_string.argtypes = [ctypes.c_int]
         L.rope_attn_status_string.restype = ctypes.c_char_p
+        R, W, C = (ctypes.POINTER(x) for x in (RaRotary, RaRows, RaCache))
+        i64, i32 = ctypes.c_int64, ctypes.c_int32
+        L.rope_attn_rotary_freqs.argtypes = [R, vp, vp, vp]
+        L.rope_attn_rotary_freqs.restype = ctypes.c_int
+        L.rope_attn_rotary.argtypes = [R, i64, i64, i32, vp, vp, W, W, W, W, vp]
+        L.rope_attn_rotary.restype = ctypes.c_int
+        L.rope_attn_rotary_workspace_bytes.argtypes = [R]
+        L.rope_attn_rotary_workspace_bytes.restype = sz
+        L.rope_attn_rotary_bwd.argtypes = [R, i64, i64, i32, vp, vp, W, W, W, W, W, W, vp, vp, sz,
+                                           vp]
+        L.rope_attn_rotary_bwd.restype = ctypes.c_int
+        L.rope_attn_cache_block_bytes.argtypes = [i64]
+        L.rope_attn_cache_block_bytes.restype = sz
+        L.rope_attn_cache_bytes.argtypes = [C]
+        L.rope_attn_cache_bytes.restype = sz
+        L.rope_attn_cache_workspace_bytes.argtypes = [C]
+        L.rope_attn_cache_workspace_bytes.restype = sz
+        L.rope_attn_cache_append.argtypes = [C, vp, vp, vp, vp, R, vp, W, W, W, W, vp, sz, vp]
+        L.rope_attn_cache_append.restype = ctypes.c_int
+        L.rope_attn_cache_read.argtypes = [C, vp, vp, vp, vp, W, W, vp, sz, vp]
+        L.rope_attn_cache_read.restype = ctypes.c_int
+        L.rope_attn_cache_attn.argtypes = [C, vp, vp, vp, vp, W, vp, vp, vp, sz, vp]
+        L.rope_attn_cache_attn.restype = ctypes.c_int
         L.rope_attn_timing_enable.argtypes = [ctypes.c_int]
         L.rope_attn_timing_enable.restype = None
         L.rope_attn_timing_read.argtypes = [ctypes.POINTER(ctypes.c_int32),
@@ -333,6 +378,275 @@ def rope_attn_alpha_adam(alpha, dalpha, m1, m2, step, lr, beta1=0.9, beta2=0.999
         ctypes.byref(opt), alpha.numel(), _ptr(alpha), _ptr(dalpha), _ptr(m1), _ptr(m2),
         _stream(alpha.device)))
     return alpha, m1, m2
+
+
+# ---------------------------------------------------------------- rotation, paged cache
+def _serving_device(fn, t):
+    """The CUDA device of t (the calls below take device memory only)."""
+    if t.device.type != "cuda":
+        raise ValueError(f"{fn}: tensors must be on a CUDA device, got {t.device}")
+    return t.device
+
+
+def _call(fn, device, *args):
+    """fn(*args, stream) with the tensors' device current (kernels launch on it)."""
+    if torch.cuda.current_device() == device.index:
+        code = getattr(lib(), fn)(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            code = getattr(lib(), fn)(*args, _stream(device))
+    if code != 0:
+        raise RopeAttnError(fn, code)
+
+
+def _vector(fn, name, t, device, dtype, shape):
+    """A contiguous tensor of the given type and shape on `device`."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or \
+            not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape "
+                         f"{tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} "
+                         f"(strides {t.stride()}) on {t.device}")
+
+
+def _head_rows(fn, name, t, device, dtype, shape):
+    """RaRows of [B, H, n, d] (4 dimensions) or [T, H, d] (3): any strides, channels
+    contiguous."""
+    if t.dtype != dtype or t.device != device or t.shape != shape:
+        raise ValueError(f"{fn}: {name} must be {dtype} of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{fn}: {name} must have contiguous channels, got strides {st}")
+    if len(shape) == 4:
+        return RaRows(t.data_ptr(), shape[1], st[0], st[1], st[2])
+    return RaRows(t.data_ptr(), shape[1], 0, st[1], st[0])
+
+
+def _opt(rows):
+    return ctypes.byref(rows) if rows is not None else None
+
+
+def rotary_spec(d, base=10000.0, rot_dim=None, layout="interleaved", scaling="none", factor=1.0,
+                orig_len=0.0, slow=1.0, fast=32.0, amplitude=1.0, fixed_bands=0):
+    """How positions turn a head of d channels: the first rot_dim (default all) of them, in the
+    "interleaved" (2m, 2m+1) or "half" (m, m + rot_dim/2) layout, with frequencies scaled by
+    "none", "linear" or "parts" (see include/rope_attn.h)."""
+    if layout not in LAYOUTS:
+        raise ValueError(f"rotary_spec: layout must be one of {sorted(LAYOUTS)}, got {layout!r}")
+    if scaling not in SCALINGS:
+        raise ValueError(f"rotary_spec: scaling must be one of {sorted(SCALINGS)}, got "
+                         f"{scaling!r}")
+    return RaRotary(int(d), int(d if rot_dim is None else rot_dim), float(base), float(factor),
+                    float(orig_len), float(slow), float(fast), float(amplitude), LAYOUTS[layout],
+                    SCALINGS[scaling], int(fixed_bands), 0)
+
+
+def rope_attn_rotary_freqs(spec, alpha=None, freqs=None, device=None):
+    """fp64 [rot_dim/2] frequencies theta_hat of `spec` with the learned log-frequency offsets
+    alpha (fp32 [rot_dim/2]; None: zeros, on `device`).  Kept by the caller for the calls below;
+    computed anew whenever alpha changes."""
+    fn = "rope_attn_rotary_freqs"
+    half = spec.rot_dim // 2
+    ref = alpha if alpha is not None else freqs
+    if ref is None:
+        ref = freqs = torch.empty(half, dtype=torch.float64, device=device or "cuda")
+    dev = _serving_device(fn, ref)
+    if alpha is not None:
+        _vector(fn, "alpha", alpha, dev, torch.float32, (half,))
+    if freqs is None:
+        freqs = torch.empty(half, dtype=torch.float64, device=dev)
+    _vector(fn, "freqs", freqs, dev, torch.float64, (half,))
+    _call(fn, dev, ctypes.byref(spec), _ptr(alpha), _ptr(freqs))
+    return freqs
+
+
+def _rotary_args(fn, spec, freqs, x, pos):
+    if x.dim() != 4 or x.dtype not in _DTYPE or x.shape[-1] != spec.d:
+        raise ValueError(f"{fn}: tensors must be [B, H, n, {spec.d}] in float32 or bfloat16, got "
+                         f"{x.dtype} {tuple(x.shape)}")
+    dev = _serving_device(fn, x)
+    B, _, n, _ = x.shape
+    _vector(fn, "freqs", freqs, dev, torch.float64, (spec.rot_dim // 2,))
+    if pos is not None:
+        _vector(fn, "pos", pos, dev, torch.int32, (B, n))
+    return dev, B, n
+
+
+def _same_tokens(fn, name, t, x):
+    if t.dim() != 4 or t.shape[0] != x.shape[0] or t.shape[2:] != x.shape[2:]:
+        raise ValueError(f"{fn}: {name} must match q in batch, tokens and channels, got "
+                         f"{tuple(t.shape)} beside {tuple(x.shape)}")
+
+
+def rope_attn_rotary(spec, freqs, q, k=None, pos=None, q_out=None, k_out=None):
+    """(q~, k~): q [B, Hq, n, d] and k [B, Hk, n, d] (any strides, channels contiguous; k may be
+    None) rotated at positions pos (int32 [B, n]; None: 0..n-1).  q_out may be q, k_out k."""
+    fn = "rope_attn_rotary"
+    dev, B, n = _rotary_args(fn, spec, freqs, q, pos)
+    q_out = torch.empty_like(q) if q_out is None else q_out
+    rows = [_head_rows(fn, "q", q, dev, q.dtype, q.shape),
+            _head_rows(fn, "q_out", q_out, dev, q.dtype, q.shape), None, None]
+    if k is not None:
+        _same_tokens(fn, "k", k, q)
+        k_out = torch.empty_like(k) if k_out is None else k_out
+        rows[2] = _head_rows(fn, "k", k, dev, q.dtype, k.shape)
+        rows[3] = _head_rows(fn, "k_out", k_out, dev, q.dtype, k.shape)
+    _call(fn, dev, ctypes.byref(spec), B, n, _DTYPE[q.dtype], _ptr(freqs), _ptr(pos),
+          *[_opt(r) for r in rows])
+    return q_out, k_out if k is not None else None
+
+
+def rope_attn_rotary_workspace_bytes(spec):
+    return int(lib().rope_attn_rotary_workspace_bytes(ctypes.byref(spec)))
+
+
+def rope_attn_rotary_bwd(spec, freqs, dq_rot, dk_rot=None, q=None, k=None, pos=None, dq=None,
+                         dk=None, dalpha=None, ws=None, frozen_alpha=False):
+    """(dq, dk, dalpha) from the gradients dq_rot, dk_rot of the rotated tensors.  q and k (the
+    forward's inputs) are needed for dalpha only; frozen_alpha: None is returned in its place."""
+    fn = "rope_attn_rotary_bwd"
+    dev, B, n = _rotary_args(fn, spec, freqs, dq_rot, pos)
+    dt = dq_rot.dtype
+    dq = torch.empty_like(dq_rot) if dq is None else dq
+    rows = [_head_rows(fn, "dq_rot", dq_rot, dev, dt, dq_rot.shape),
+            _head_rows(fn, "dq", dq, dev, dt, dq_rot.shape), None, None, None, None]
+    if dk_rot is not None:
+        _same_tokens(fn, "dk_rot", dk_rot, dq_rot)
+        dk = torch.empty_like(dk_rot) if dk is None else dk
+        rows[2] = _head_rows(fn, "dk_rot", dk_rot, dev, dt, dk_rot.shape)
+        rows[3] = _head_rows(fn, "dk", dk, dev, dt, dk_rot.shape)
+    if frozen_alpha:
+        dalpha = ws = None
+    else:
+        if q is None or (k is None) != (dk_rot is None):
+            raise ValueError(f"{fn}: dalpha needs the forward's q (and k, if it had one); pass "
+                             "frozen_alpha=True for none")
+        rows[4] = _head_rows(fn, "q", q, dev, dt, dq_rot.shape)
+        if dk_rot is not None:
+            rows[5] = _head_rows(fn, "k", k, dev, dt, dk_rot.shape)
+        half = spec.rot_dim // 2
+        if dalpha is None:
+            dalpha = torch.empty(half, dtype=torch.float32, device=dev)
+        _vector(fn, "dalpha", dalpha, dev, torch.float32, (half,))
+        if ws is None:
+            ws = torch.empty(rope_attn_rotary_workspace_bytes(spec), dtype=torch.uint8,
+                             device=dev)
+        _vector(fn, "ws", ws, dev, torch.uint8, (ws.numel(),))
+    _call(fn, dev, ctypes.byref(spec), B, n, _DTYPE[dt], _ptr(freqs), _ptr(pos),
+          *[_opt(r) for r in rows], _ptr(dalpha), _ptr(ws), ws.numel() if ws is not None else 0)
+    return dq, dk if dk_rot is not None else None, dalpha
+
+
+def cache_plan(B, T, Hq, Hkv, d, dtype, pages, page_size, max_pages, causal=True, window=0,
+               scale=0.0, max_q=0):
+    """A batch of B sequences with T new tokens over a 4-bit cache of `pages` pages (see
+    include/rope_attn.h: ra_cache).  max_q: most new tokens of one sequence (0: T)."""
+    if isinstance(dtype, torch.dtype):
+        dtype = _DTYPE[dtype]
+    return RaCache(int(B), int(T), int(Hq), int(Hkv), int(d), int(pages), int(page_size),
+                   int(max_pages), int(max_q), int(window), float(scale), int(dtype),
+                   int(bool(causal)))
+
+
+def rope_attn_cache_block_bytes(d):
+    return int(lib().rope_attn_cache_block_bytes(int(d)))
+
+
+def rope_attn_cache_bytes(plan):
+    return int(lib().rope_attn_cache_bytes(ctypes.byref(plan)))
+
+
+def rope_attn_cache_workspace_bytes(plan):
+    return int(lib().rope_attn_cache_workspace_bytes(ctypes.byref(plan)))
+
+
+def cache_workspace(plan, device):
+    """A device workspace for the cache calls on `plan`, its error word zeroed."""
+    nbytes = rope_attn_cache_workspace_bytes(plan)
+    if nbytes == 0:
+        raise RopeAttnError("rope_attn_cache_workspace_bytes", 1)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws[:64].zero_()
+    return ws
+
+
+def new_cache(plan, device):
+    """A zeroed cache [pages, Hkv, page_size / 16, block bytes] (uint8) for `plan`."""
+    if rope_attn_cache_bytes(plan) == 0:
+        raise RopeAttnError("rope_attn_cache_bytes", 1)
+    return torch.zeros((plan.pages, plan.Hkv, plan.page_size // 16,
+                        rope_attn_cache_block_bytes(plan.d)), dtype=torch.uint8, device=device)
+
+
+_CACHE_DTYPE = {RA_F32: torch.float32, RA_BF16: torch.bfloat16}
+
+
+def _cache_args(fn, plan, cache, table, indptr, kv_len, ws):
+    dev = _serving_device(fn, cache)
+    if cache.dtype != torch.uint8 or not cache.is_contiguous() or \
+            cache.numel() != rope_attn_cache_bytes(plan):
+        raise ValueError(f"{fn}: cache must be a contiguous uint8 tensor of "
+                         f"{rope_attn_cache_bytes(plan)} bytes, got {cache.dtype} "
+                         f"{tuple(cache.shape)} (strides {cache.stride()})")
+    _vector(fn, "table", table, dev, torch.int32, (plan.B, plan.max_pages))
+    _vector(fn, "indptr", indptr, dev, torch.int32, (plan.B + 1,))
+    _vector(fn, "kv_len", kv_len, dev, torch.int32, (plan.B,))
+    if ws is None:
+        ws = cache_workspace(plan, dev)
+    _vector(fn, "ws", ws, dev, torch.uint8, (ws.numel(),))
+    return dev, ws, (ctypes.byref(plan), _ptr(cache), _ptr(table), _ptr(indptr), _ptr(kv_len))
+
+
+def rope_attn_cache_append(plan, cache, table, indptr, kv_len, spec, freqs, k, v, q=None,
+                           q_out=None, ws=None):
+    """Write the batch's k (rotated by spec and freqs at its positions) and v [T, Hkv, d] into
+    the cache; returns q [T, Hq, d] rotated at the same positions (None without q).  kv_len
+    counts the appended tokens already.  Device-side faults (a bad page, length or offset, a
+    value beyond the cache's range) stay in ws for rope_attn_device_status."""
+    fn = "rope_attn_cache_append"
+    dev, ws, head = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)
+    dt = _CACHE_DTYPE[plan.dtype]
+    kv = torch.Size((plan.T, plan.Hkv, plan.d))
+    _vector(fn, "freqs", freqs, dev, torch.float64, (spec.rot_dim // 2,))
+    rows = [_head_rows(fn, "k", k, dev, dt, kv), _head_rows(fn, "v", v, dev, dt, kv), None, None]
+    if q is not None:
+        qs = torch.Size((plan.T, plan.Hq, plan.d))
+        rows[2] = _head_rows(fn, "q", q, dev, dt, qs)
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        rows[3] = _head_rows(fn, "q_out", q_out, dev, dt, qs)
+    _call(fn, dev, *head, ctypes.byref(spec), _ptr(freqs), *[_opt(r) for r in rows], _ptr(ws),
+          ws.numel())
+    return q_out if q is not None else None
+
+
+def rope_attn_cache_read(plan, cache, table, indptr, kv_len, k=None, v=None, ws=None):
+    """(k, v) [T, Hkv, d]: the cached rows of the batch's tokens as the values they stand for
+    (for a whole cache, give indptr the running sum of kv_len)."""
+    fn = "rope_attn_cache_read"
+    dev, ws, head = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)
+    dt = _CACHE_DTYPE[plan.dtype]
+    kv = torch.Size((plan.T, plan.Hkv, plan.d))
+    k = torch.empty(kv, dtype=dt, device=dev) if k is None else k
+    v = torch.empty(kv, dtype=dt, device=dev) if v is None else v
+    rows = [_head_rows(fn, "k", k, dev, dt, kv), _head_rows(fn, "v", v, dev, dt, kv)]
+    _call(fn, dev, *head, *[_opt(r) for r in rows], _ptr(ws), ws.numel())
+    return k, v
+
+
+def rope_attn_cache_attn(plan, cache, table, indptr, kv_len, q, o=None, lse=None, ws=None):
+    """(o [T, Hq, d], lse fp32 [T, Hq]): attention of the rotated queries q [T, Hq, d] over the
+    cache.  Rows that belong to no sequence are left as they were."""
+    fn = "rope_attn_cache_attn"
+    dev, ws, head = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)
+    dt = _CACHE_DTYPE[plan.dtype]
+    qs = torch.Size((plan.T, plan.Hq, plan.d))
+    rows = _head_rows(fn, "q", q, dev, dt, qs)
+    o = torch.empty(qs, dtype=dt, device=dev) if o is None else o
+    lse = torch.empty((plan.T, plan.Hq), dtype=torch.float32, device=dev) if lse is None else lse
+    _vector(fn, "o", o, dev, dt, qs)
+    _vector(fn, "lse", lse, dev, torch.float32, (plan.T, plan.Hq))
+    _call(fn, dev, *head, ctypes.byref(rows), _ptr(o), _ptr(lse), _ptr(ws), ws.numel())
+    return o, lse
 
 
 def rope_attn_device_status(ws):

@@ -236,6 +236,7 @@ const char* rope_attn_status_string(ra_status s) {
     case RA_ERR_CUDA: return "CUDA error";
     case RA_ERR_TIMEOUT: return "device-side wait timed out";
     case RA_ERR_RANGE: return "input entry beyond the fp16 range of the score operands";
+    case RA_ERR_CACHE: return "page, length or offset outside the cache or the batch";
   }
   return "unknown status";
 }
@@ -404,6 +405,7 @@ ra_status rope_attn_device_status(void* ws, size_t ws_bytes, void* stream, int32
     info[2] = (int32_t)word[3];
   }
   if (word[0] == 0) return RA_OK;
+  if (word[0] == (uint32_t)RA_ERR_CACHE) return RA_ERR_CACHE;
   return word[0] == (uint32_t)RA_ERR_RANGE ? RA_ERR_RANGE : RA_ERR_TIMEOUT;
 }
 
@@ -446,7 +448,10 @@ const char* rope_attn_kernel_name(int id) {
       "loss_partial",     "loss_final",   "bwd_delta",    "bwd_dq_f32",
       "bwd_dkdv_f32",     "bwd_dq_sm100", "bwd_dkdv_sm100", "dalpha_final",
       "proj_gemm",        "proj_dw_gemm", "proj_dx_gemm", "merge_heads",
-      "spectrum",         "alpha_adam"};
+      "spectrum",         "alpha_adam",   "unknown",      "rotary_freqs",
+      "rotary",           "rotary_bwd",   "rotary_dalpha", "cache_append",
+      "cache_read",       "cache_attn_f32", "cache_attn", "cache_attn_chunk",
+      "cache_combine"};
   return (id >= 0 && id < K_COUNT) ? names[id] : "unknown";
 }
 

@@ -1,0 +1,396 @@
+// cache_attn.cu -- attention over the paged 4-bit cache: the fp32 kernel, the combine kernel
+// and the entry point.
+//
+//   o_i = sum_j p_ij v_j / l_i,  p_ij = 2^(s_ij - m_i),  s_ij = scale log2(e) q_i . k_j
+//
+// over the keys that row i sees, with the running maximum m and sum l of an online softmax, one
+// pass over the cache ("RoPE attention can be trained in almost-linear time", Metodologia 1:
+// the normalised softmax).  k_j and v_j are lo + step * code of the stored codes.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math_constants.h>
+
+#include "cache_attn.h"
+#include "cache_sched.cuh"
+#include "common.h"
+#include "launch.h"
+#include "rope.cuh"
+
+namespace ra {
+namespace {
+
+// ------------------------------------------------------------------ fp32, CUDA cores
+// A block of 4 warps takes one row tile (R rows) of an item; in a step of 128 keys each warp
+// takes 32.  Scores: a lane owns a key and reads its whole row of codes (16-byte loads), the
+// queries come as broadcasts from shared memory.  Values: a lane owns D / 32 channels and the
+// warp walks the 32 keys, the weights coming as broadcasts.  Everything is fp32: a code becomes
+// the float 2^23 + code by or-ing it under that exponent, minus 2^23 (both exact), and
+// lo + step * code is rounded once.
+constexpr int kF32Threads = 128;
+
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const AttnArgs a) {
+  constexpr int DL = D / 32;  // channels of a lane in the value product
+  __shared__ __align__(16) float q_s[R][D];
+  __shared__ __align__(16) float p_s[4][32][R];
+  __shared__ float o_s[4][R][D];
+  __shared__ float ml_s[4][R][2];
+  __shared__ long long scratch[8];
+  const CacheDims& c = a.c;
+  const int G = c.Hq / c.Hkv;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const float scale_log2 = c.scale * 1.4426950408889634f;
+
+  const Run run = find_run(a, scratch, K_CACHE_ATTN_F32);
+  Walk<WorkOf> walk(WorkOf{a}, run, c.B);
+  Segment s;
+  int followers = 0, fb = 0, fh = 0, ft = 0;
+  while (walk.next(s)) {
+    const long long row0 = (long long)s.tile * R;
+    const int rows = (int)min((long long)R, (long long)s.w.qn * G - row0);
+    for (int i = threadIdx.x; i < R * D; i += kF32Threads) {
+      const int r = i / D, ch = i % D;
+      float x = 0.f;
+      if (r < rows) {
+        const long long row = row0 + r;
+        const T* src = static_cast<const T*>(a.q) + (s.w.q0 + row / G) * a.q_n +
+                       ((long long)s.h * G + row % G) * a.q_h;
+        Vec<T, 1> v;
+        float f[1];
+        v.load(src + ch);
+        v.get(f);
+        x = f[0] * scale_log2;
+      }
+      q_s[r][ch] = x;
+    }
+    __syncthreads();
+    float m[R], l[R], o[R][DL];
+    KeyRange kr[R];
+    int lo_all = s.w.L, hi_all = 0;  // keys that any row of the tile sees
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = -CUDART_INF_F;
+      l[r] = 0.f;
+#pragma unroll
+      for (int e = 0; e < DL; ++e) o[r][e] = 0.f;
+      kr[r] = r < rows ? row_keys(c, s.w, row0 + r, G) : KeyRange{0, 0};
+      if (kr[r].lo < kr[r].hi) {
+        lo_all = min(lo_all, kr[r].lo);
+        hi_all = max(hi_all, kr[r].hi);
+      }
+    }
+    for (int step = s.s0; step < s.s1; ++step) {
+      const int k0 = s.w.first + step * kStep + warp * 32;
+      if (k0 >= hi_all || k0 + 32 <= lo_all) continue;
+      const int key = k0 + lane;
+      const uint8_t* block = nullptr;  // of this lane's key
+      if (key < s.w.L) {
+        const int page = page_of(c, a.table, s.b, key / kBlock, a.err, K_CACHE_ATTN_F32);
+        if (page >= 0) block = a.cache + block_at(c, page, s.h, (key / kBlock) % c.page_blocks);
+      }
+      float sc[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) sc[r] = 0.f;
+      if (block) {
+        const uint4* codes = reinterpret_cast<const uint4*>(block + (key % kBlock) * (D / 2));
+        const __half2* pairs =
+            reinterpret_cast<const __half2*>(block + code_bytes(D)) + (key % kBlock) * (D / kGroup);
+#pragma unroll 1
+        for (int g = 0; g < D / kGroup; ++g) {
+          const float2 pr = __half22float2(pairs[g]);
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const uint4 w4 = codes[2 * g + v];
+            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float k[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                k[j] = fmaf(pr.x,
+                            __uint_as_float(((w[e] >> (4 * j)) & 15u) | 0x4b000000u) - 8388608.f,
+                            pr.y);
+#pragma unroll
+              for (int r = 0; r < R; ++r) {
+                const float4* qv =
+                    reinterpret_cast<const float4*>(&q_s[r][g * 64 + v * 32 + e * 8]);
+                const float4 q0 = qv[0], q1 = qv[1];
+                sc[r] = fmaf(k[0], q0.x, sc[r]);
+                sc[r] = fmaf(k[1], q0.y, sc[r]);
+                sc[r] = fmaf(k[2], q0.z, sc[r]);
+                sc[r] = fmaf(k[3], q0.w, sc[r]);
+                sc[r] = fmaf(k[4], q1.x, sc[r]);
+                sc[r] = fmaf(k[5], q1.y, sc[r]);
+                sc[r] = fmaf(k[6], q1.z, sc[r]);
+                sc[r] = fmaf(k[7], q1.w, sc[r]);
+              }
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float x = block && key >= kr[r].lo && key < kr[r].hi ? sc[r] : -CUDART_INF_F;
+        float mx = x;
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+        const float m_new = fmaxf(m[r], mx);
+        float p = 0.f;
+        if (m_new != -CUDART_INF_F) {
+          const float corr = exp2f(m[r] - m_new);
+          p = exp2f(x - m_new);
+          l[r] = l[r] * corr + p;
+#pragma unroll
+          for (int e = 0; e < DL; ++e) o[r][e] *= corr;
+          m[r] = m_new;
+        }
+        p_s[warp][lane][r] = p;
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const uint8_t* vb = reinterpret_cast<const uint8_t*>(__shfl_sync(
+            0xffffffffu, reinterpret_cast<unsigned long long>(block), half * 16));
+        if (!vb) continue;
+        vb += value_offset(D);
+        const int n = min(16, s.w.L - (k0 + half * 16));
+        const __half2* pairs = reinterpret_cast<const __half2*>(vb + code_bytes(D)) +
+                               (lane * DL) / kGroup;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+          uint32_t w;
+          if constexpr (DL == 4) w = reinterpret_cast<const uint16_t*>(vb + j * (D / 2))[lane];
+          else w = vb[j * (D / 2) + lane];
+          const float2 pr = __half22float2(pairs[j * (D / kGroup)]);
+          float v[DL];
+#pragma unroll
+          for (int e = 0; e < DL; ++e)
+            v[e] = fmaf(pr.x, __uint_as_float(((w >> (4 * e)) & 15u) | 0x4b000000u) - 8388608.f,
+                        pr.y);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float p = p_s[warp][half * 16 + j][r];
+#pragma unroll
+            for (int e = 0; e < DL; ++e) o[r][e] = fmaf(p, v[e], o[r][e]);
+          }
+        }
+      }
+      __syncwarp();
+    }
+    // the four warps' partial softmaxes joined in order
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], w);
+      if (lane == 0) {
+        ml_s[warp][r][0] = m[r];
+        ml_s[warp][r][1] = l[r];
+      }
+#pragma unroll
+      for (int e = 0; e < DL; ++e) o_s[warp][r][lane * DL + e] = o[r][e];
+    }
+    __syncthreads();
+    const bool whole = s.first && s.last;
+    const long long slot = 2ll * blockIdx.x + (s.first ? 1 : 0);
+    for (int i = threadIdx.x; i < rows * D; i += kF32Threads) {
+      const int r = i / D, ch = i % D;
+      float mx = -CUDART_INF_F;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mx = fmaxf(mx, ml_s[w][r][0]);
+      float sum = 0.f, wl = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = mx == -CUDART_INF_F ? 0.f : exp2f(ml_s[w][r][0] - mx);
+        sum = fmaf(f, o_s[w][r][ch], sum);
+        wl = fmaf(f, ml_s[w][r][1], wl);
+      }
+      if (whole) {
+        const long long row = row0 + r;
+        const long long at = (s.w.q0 + row / G) * c.Hq + (long long)s.h * G + row % G;
+        Vec<T, 1> v;
+        const float f[1] = {wl > 0.f ? sum / wl : 0.f};
+        v.set(f);
+        v.store(static_cast<T*>(a.o) + at * D + ch);
+        if (ch == 0) a.lse[at] = (mx + log2f(wl)) * 0.6931471805599453f;
+      } else {
+        a.acc[(slot * a.tile + r) * D + ch] = sum;
+        if (ch == 0) {
+          a.ml[(slot * a.tile + r) * 2] = mx;
+          a.ml[(slot * a.tile + r) * 2 + 1] = wl;
+        }
+      }
+    }
+    if (s.followers) followers = s.followers, fb = s.b, fh = s.h, ft = s.tile;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) a.desc[blockIdx.x] = PartDesc{followers, fb, fh, ft};
+}
+
+// ------------------------------------------------------------------ joining split items
+// Block (c, r): row r (and every gridDim.y-th after it) of the split item that begins in block
+// c of the attention launch.  8 warps share the parts, a lane D / 32 channels.
+constexpr int kCombineThreads = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kCombineThreads) cache_combine_kernel(const AttnArgs a) {
+  constexpr int DL = D / 32;
+  __shared__ float red[8][D], red_l[8];
+  __shared__ float mx_s[8];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const PartDesc d = a.desc[blockIdx.x];
+  if (d.followers == 0) return;
+  const CacheDims& c = a.c;
+  const int G = c.Hq / c.Hkv, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const SeqWork w = load_work(a, d.b);
+  const long long row0 = (long long)d.tile * a.tile;
+  const int rows = (int)min((long long)a.tile, (long long)w.qn * G - row0);
+  const int parts = d.followers + 1;
+  // part 0 is the beginning block's "goes on" slot, part k > 0 block c + k's "came over" slot
+  auto slot_of = [&](int k) { return 2ll * (blockIdx.x + k) + (k == 0 ? 1 : 0); };
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    float mx = -CUDART_INF_F;
+    for (int k = threadIdx.x; k < parts; k += kCombineThreads)
+      mx = fmaxf(mx, a.ml[(slot_of(k) * a.tile + r) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane == 0) mx_s[warp] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mx = fmaxf(mx, mx_s[k]);
+    float acc[DL], l = 0.f;
+#pragma unroll
+    for (int e = 0; e < DL; ++e) acc[e] = 0.f;
+    if (mx != -CUDART_INF_F) {
+#pragma unroll 4
+      for (int k = warp; k < parts; k += 8) {
+        const long long at = slot_of(k) * a.tile + r;
+        const float f = exp2f(a.ml[at * 2] - mx);
+        l = fmaf(f, a.ml[at * 2 + 1], l);
+        const float* src = a.acc + at * D + lane * DL;
+#pragma unroll
+        for (int e = 0; e < DL; ++e) acc[e] = fmaf(f, src[e], acc[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < DL; ++e) red[warp][lane * DL + e] = acc[e];
+    if (lane == 0) red_l[warp] = l;
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float sum = 0.f, wl = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        sum += red[k][threadIdx.x];
+        wl += red_l[k];
+      }
+      const long long row = row0 + r;
+      const long long at = (w.q0 + row / G) * c.Hq + (long long)d.h * G + row % G;
+      Vec<T, 1> v;
+      const float f[1] = {wl > 0.f ? sum / wl : 0.f};
+      v.set(f);
+      v.store(static_cast<T*>(a.o) + at * D + threadIdx.x);
+      if (threadIdx.x == 0) a.lse[at] = (mx + log2f(wl)) * 0.6931471805599453f;
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_f32(AttnArgs& a, int rows, cudaStream_t s) {
+  // the smallest tile that holds the rows of the longest sequence
+  if (rows <= 1) {
+    a.tile = 1;
+    cache_attn_f32_kernel<T, D, 1><<<kRowsBlocks, kF32Threads, 0, s>>>(a);
+  } else if (rows <= 2) {
+    a.tile = 2;
+    cache_attn_f32_kernel<T, D, 2><<<kRowsBlocks, kF32Threads, 0, s>>>(a);
+  } else if (rows <= 4) {
+    a.tile = 4;
+    cache_attn_f32_kernel<T, D, 4><<<kRowsBlocks, kF32Threads, 0, s>>>(a);
+  } else {
+    a.tile = 8;
+    cache_attn_f32_kernel<T, D, 8><<<kRowsBlocks, kF32Threads, 0, s>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// The combine launch overlaps its start with the attention kernel's end (programmatic stream
+// serialisation: it waits for that kernel's writes before it reads any).
+cudaError_t launch_cache_combine(const AttnArgs& a, int blocks, int32_t dtype, int rows,
+                                 cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)blocks, (unsigned)std::min(rows, 64));
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (dtype == RA_BF16)
+    return a.c.d == 64 ? cudaLaunchKernelEx(&cfg, cache_combine_kernel<__nv_bfloat16, 64>, a)
+                       : cudaLaunchKernelEx(&cfg, cache_combine_kernel<__nv_bfloat16, 128>, a);
+  return a.c.d == 64 ? cudaLaunchKernelEx(&cfg, cache_combine_kernel<float, 64>, a)
+                     : cudaLaunchKernelEx(&cfg, cache_combine_kernel<float, 128>, a);
+}
+
+}  // namespace ra
+
+using namespace ra;
+
+extern "C" {
+
+size_t rope_attn_cache_workspace_bytes(const ra_cache* p) {
+  if (check_cache(p) != RA_OK) return 0;
+  return cache_ws(kRowsBlocks, kRowsTile, (int)p->d).total;
+}
+
+ra_status rope_attn_cache_attn(const ra_cache* p, const void* cache, const int32_t* table,
+                               const int32_t* indptr, const int32_t* kv_len, const ra_rows* q,
+                               void* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  ra_status st = check_cache_call(p, cache, table, indptr, kv_len, ws, ws_bytes);
+  if (st != RA_OK) return st;
+  if (p->T == 0) return RA_OK;
+  const size_t elem = elem_bytes(p->dtype);
+  const int64_t V = (int64_t)(16 / elem);
+  if (!q || !q->ptr || (uintptr_t)q->ptr % elem || q->H != p->Hq || q->stride_n < 0 ||
+      q->stride_h < 0 || q->stride_n > (int64_t(1) << 40) || q->stride_h > (int64_t(1) << 40))
+    return RA_ERR_INVALID_ARG;
+  if (!o || (uintptr_t)o % 16 || !lse || (uintptr_t)lse % 4) return RA_ERR_INVALID_ARG;
+  AttnArgs a{};
+  a.c = cache_dims(*p);
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.table = table, a.indptr = indptr, a.kv_len = kv_len;
+  a.q = q->ptr, a.q_n = q->stride_n, a.q_h = q->stride_h;
+  a.q_vec = (uintptr_t)q->ptr % 16 == 0 && q->stride_n % V == 0 && q->stride_h % V == 0;
+  a.o = o, a.lse = lse;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  a.err = reinterpret_cast<uint32_t*>(base);
+  a.wait_ns = wait_limit_ns();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t most_rows = (int64_t)a.c.max_q * (p->Hq / p->Hkv);  // of one sequence and head
+
+  const CacheWs w = cache_ws(kRowsBlocks, kRowsTile, a.c.d);
+  a.desc = reinterpret_cast<PartDesc*>(base + w.desc);
+  a.ml = reinterpret_cast<float*>(base + w.ml);
+  a.acc = reinterpret_cast<float*>(base + w.acc);
+  a.min_rows = 0, a.max_rows = int64_t(1) << 62;
+  a.min_steps = 2;
+  const int rows = (int)std::min<int64_t>(most_rows, 8);
+  cudaError_t e;
+  {
+    const TimingScope timed(K_CACHE_ATTN_F32, s);
+    if (p->dtype == RA_BF16)
+      e = p->d == 64 ? launch_f32<__nv_bfloat16, 64>(a, rows, s)
+                     : launch_f32<__nv_bfloat16, 128>(a, rows, s);
+    else
+      e = p->d == 64 ? launch_f32<float, 64>(a, rows, s) : launch_f32<float, 128>(a, rows, s);
+  }
+  if (e != cudaSuccess) return RA_ERR_CUDA;
+  const TimingScope timed(K_CACHE_COMBINE, s);
+  e = launch_cache_combine(a, kRowsBlocks, p->dtype, (int)std::min<int64_t>(most_rows, a.tile), s);
+  return e == cudaSuccess ? RA_OK : RA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -27,7 +27,18 @@ enum KernelId : int {
   K_MERGE_HEADS = 15,
   K_SPECTRUM = 16,
   K_ALPHA_ADAM = 17,
-  K_COUNT = 18
+  // 18 is not assigned (rope_attn_kernel_name calls it "unknown")
+  K_ROTARY_FREQS = 19,
+  K_ROTARY = 20,
+  K_ROTARY_BWD = 21,
+  K_ROTARY_DALPHA = 22,
+  K_CACHE_APPEND = 23,
+  K_CACHE_READ = 24,
+  K_CACHE_ATTN_F32 = 25,
+  K_CACHE_ATTN = 26,        // a few rows per sequence, mma.sync
+  K_CACHE_ATTN_CHUNK = 27,  // chunks of rows, tcgen05
+  K_CACHE_COMBINE = 28,
+  K_COUNT = 29
 };
 
 // Rows per dalpha partial (one partial per band per tile of query or key rows).

@@ -1,0 +1,439 @@
+// rotary.cu -- the rotation outside the attention step: frequencies of a layout, rotation of
+// q and k at given positions, and its gradients.
+//
+//   theta_hat_m = e^alpha_m s_m(base^(-2m/r)),  y = A R(p theta_hat) x on the first r channels
+//   dx = A R(-p theta_hat) dy,  dalpha_m = theta_hat_m sum_rows p <dx_m, J x_m>
+//
+// ("LeRoPE: learnable RoPE frequencies", Mecanismo Central and Declaracao do Problema: learned
+// exponential rescaling, rotation in 2-D frequency bands.)
+//
+// Both directions are bound by HBM: every element is read once and written once (the backward
+// reads the rotated part of x besides), a few operations each.  The angles are the other cost:
+// fp64, one (cos, sin) per token and band whatever the number of heads.  A thread therefore
+// keeps one token and one 16-byte unit of the head (two for the half layout: channel m goes
+// with m + r/2), forms their cos and sin once in registers, and walks the heads with four
+// vectors in flight.  The offsets' gradient is summed in fp64 registers over the heads and
+// tokens of a thread, over the block in shared memory, and over the blocks by a second small
+// kernel, always in the same order.
+#include <cmath>
+
+#include "common.h"
+#include "launch.h"
+#include "rope.cuh"
+#include "serving.h"
+
+namespace ra {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;  // heads in flight per thread
+
+struct HeadRows {      // one tensor of the call
+  const void* in;      // forward: x; backward: dy
+  void* out;           // forward: y; backward: dx
+  const void* x;       // backward with dalpha: the forward's input
+  int H;
+  int64_t ib, ih, in_, ob, oh, on, xb, xh, xn;  // strides of batch, head, token (elements)
+};
+
+struct RotArgs {
+  HeadRows t[2];
+  const int* pos;
+  const double* freqs;
+  double amplitude;
+  double* part;        // [gridDim.y gridDim.x][r / 2], or null
+  long long tokens;    // B n
+  int n, r, d;
+  int rot_units, units, tile;      // units of a row, tokens of a block's tile
+  int heads_per_chunk;
+};
+
+// V: elements of one access (a 16-byte vector, or 1 where sizes, strides or addresses allow
+// no vector).
+template <typename T, int V, bool HALF, bool BWD>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotArgs a) {
+  constexpr int W = HALF ? V : (V > 1 ? V : 2);      // channels of the first (or only) piece
+  constexpr int NP = HALF ? V : W / 2;               // pairs of a unit
+  constexpr int NV = HALF || V == 1 ? 2 : 1;         // accesses of a unit
+  extern __shared__ double red[];
+  const int tt = threadIdx.x / a.units, u = threadIdx.x - tt * a.units;
+  const bool rot = u < a.rot_units;
+  const int c0 = rot ? u * W : a.r + (u - a.rot_units) * V;
+  const int c1 = HALF ? c0 + a.r / 2 : c0 + 1;       // second access (rotated units only)
+  const int m0 = HALF ? c0 : c0 / 2;
+  const int lo = blockIdx.y * a.heads_per_chunk, hi = lo + a.heads_per_chunk;
+  const long long tiles = (a.tokens + a.tile - 1) / a.tile;
+  const bool torque = BWD && a.part != nullptr;
+  double acc[NP];
+#pragma unroll
+  for (int j = 0; j < NP; ++j) acc[j] = 0.0;
+
+  for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const long long tok = tile * a.tile + tt;
+    if (tt >= a.tile || tok >= a.tokens) continue;
+    const long long b = tok / a.n, i = tok - b * a.n;
+    const double p = (double)(a.pos ? a.pos[tok] : (int)i);
+    float2 cs[NP];
+    if (rot) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) cs[j] = cos_sin(p, a.freqs[m0 + j], a.amplitude);
+    }
+    double w[NP];
+#pragma unroll
+    for (int j = 0; j < NP; ++j) w[j] = 0.0;
+    int first = 0;  // heads of the tensors before this one
+#pragma unroll 1
+    for (int z = 0; z < 2; ++z) {
+      const HeadRows& t = a.t[z];
+      const int h0 = max(0, lo - first), h1 = min(t.H, hi - first);
+      first += t.H;
+      if (h0 >= h1 || (!rot && t.in == t.out)) continue;  // in place: the rest stays
+      const T* src = static_cast<const T*>(t.in) + b * t.ib + i * t.in_;
+      T* dst = static_cast<T*>(t.out) + b * t.ob + i * t.on;
+      const T* xs = torque ? static_cast<const T*>(t.x) + b * t.xb + i * t.xn : nullptr;
+      for (int h = h0; h < h1; h += kUnroll) {
+        Vec<T, V> v[kUnroll][NV], xv[BWD ? kUnroll : 1][NV];
+#pragma unroll
+        for (int e = 0; e < kUnroll; ++e) {
+          if (h + e < h1) {
+            v[e][0].load(src + (h + e) * t.ih + c0);
+            if (NV == 2 && rot) v[e][NV - 1].load(src + (h + e) * t.ih + c1);
+            if constexpr (BWD) {
+              if (torque && rot) {
+                xv[e][0].load(xs + (h + e) * t.xh + c0);
+                if (NV == 2) xv[e][NV - 1].load(xs + (h + e) * t.xh + c1);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kUnroll; ++e) {
+          if (h + e >= h1) break;
+          if (rot) {
+            // the unit's pairs: (f[0][j], f[1][j]) when it has two accesses, else neighbours
+            float f[NV][V];
+#pragma unroll
+            for (int s = 0; s < NV; ++s) v[e][s].get(f[s]);
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+              float& x0 = NV == 2 ? f[0][j] : f[0][(2 * j) % V];
+              float& x1 = NV == 2 ? f[NV - 1][j] : f[0][(2 * j + 1) % V];
+              const float2 y = BWD ? turn_back(cs[j], x0, x1) : turn(cs[j], x0, x1);
+              x0 = y.x;
+              x1 = y.y;
+            }
+            if constexpr (BWD) {
+              if (torque) {
+                float g[NV][V];
+#pragma unroll
+                for (int s = 0; s < NV; ++s) xv[e][s].get(g[s]);
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                  const float d0 = NV == 2 ? f[0][j] : f[0][(2 * j) % V];
+                  const float d1 = NV == 2 ? f[NV - 1][j] : f[0][(2 * j + 1) % V];
+                  const float x0 = NV == 2 ? g[0][j] : g[0][(2 * j) % V];
+                  const float x1 = NV == 2 ? g[NV - 1][j] : g[0][(2 * j + 1) % V];
+                  w[j] += (double)(d1 * x0 - d0 * x1);
+                }
+              }
+            }
+#pragma unroll
+            for (int s = 0; s < NV; ++s) v[e][s].set(f[s]);
+          }
+          v[e][0].store(dst + (h + e) * t.oh + c0);
+          if (NV == 2 && rot) v[e][NV - 1].store(dst + (h + e) * t.oh + c1);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NP; ++j) acc[j] += p * w[j];
+  }
+  if constexpr (BWD) {
+    if (!torque) return;
+    // red[unit][pair][token of the tile], summed over the tokens in order
+    if (tt < a.tile && rot) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) red[(u * NP + j) * a.tile + tt] = acc[j];
+    }
+    __syncthreads();
+    double* part = a.part + ((long long)blockIdx.y * gridDim.x + blockIdx.x) * (a.r / 2);
+    for (int m = threadIdx.x; m < a.r / 2; m += blockDim.x) {
+      double s = 0.0;
+      for (int k = 0; k < a.tile; ++k) s += red[m * a.tile + k];
+      part[m] = s;
+    }
+  }
+}
+
+// dalpha_m = theta_hat_m times the sum of the blocks' partial torques, fixed order.
+__global__ void __launch_bounds__(128)
+    rotary_dalpha_kernel(const double* __restrict__ part, int parts, int M,
+                         const double* __restrict__ freqs, float* __restrict__ dalpha) {
+  __shared__ double red[128];
+  const int m = blockIdx.x;
+  double s = 0.0;
+  for (int k = threadIdx.x; k < parts; k += 128) s += part[(long long)k * M + m];
+  red[threadIdx.x] = s;
+  __syncthreads();
+  for (int w = 64; w > 0; w >>= 1) {
+    if (threadIdx.x < w) red[threadIdx.x] += red[threadIdx.x + w];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) dalpha[m] = (float)(freqs[m] * red[0]);
+}
+
+__global__ void rotary_freqs_kernel(const ra_rotary r, const float* __restrict__ alpha,
+                                    double* __restrict__ freqs) {
+  const int m = blockIdx.x * blockDim.x + threadIdx.x;
+  const int M = (int)(r.rot_dim / 2);
+  if (m >= M) return;
+  double t = pow(r.base, -2.0 * (double)m / (double)r.rot_dim);
+  if (r.scaling == RA_SCALE_LINEAR) {
+    t = t / r.factor;
+  } else if (r.scaling == RA_SCALE_PARTS) {
+    // turns of the band over the original context: few -> interpolated, many -> kept
+    double g = (r.orig_len * t / 6.2831853071795864769 - r.slow) / (r.fast - r.slow);
+    g = fmin(1.0, fmax(0.0, g));
+    t = (1.0 - g) * t / r.factor + g * t;
+  }
+  if (alpha) t *= exp((double)alpha[m]);
+  freqs[m] = m >= M - r.fixed_bands ? 0.0 : t;
+}
+
+// ------------------------------------------------------------------ host
+bool aligned_to(const void* p, size_t a) {
+  return (reinterpret_cast<uintptr_t>(p) % a) == 0;
+}
+
+// Rows of a written tensor must not overlap: with the extents above 1 sorted by stride, each
+// stride clears the whole extent below it.
+bool rows_distinct(const ra_rows& r, int64_t B, int64_t n, int64_t d) {
+  int64_t ext[3] = {B, r.H, n}, st[3] = {r.stride_b, r.stride_h, r.stride_n};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (st[j] < st[i]) {
+        std::swap(st[i], st[j]);
+        std::swap(ext[i], ext[j]);
+      }
+  int64_t span = d;
+  for (int i = 0; i < 3; ++i) {
+    if (ext[i] == 1) continue;
+    if (st[i] < span) return false;
+    span = st[i] * (ext[i] - 1) + span;
+  }
+  return true;
+}
+
+ra_status check_rows(const ra_rows* r, const ra_rotary& s, int64_t B, int64_t n, int32_t dtype,
+                     bool written) {
+  if (!r || !r->ptr || !aligned_to(r->ptr, elem_bytes(dtype))) return RA_ERR_INVALID_ARG;
+  if (r->H < 1 || r->H > kMaxHeads) return RA_ERR_INVALID_ARG;
+  for (int64_t st : {r->stride_b, r->stride_h, r->stride_n})
+    if (st < 0 || st > (int64_t(1) << 40)) return RA_ERR_INVALID_ARG;
+  if (written && !rows_distinct(*r, B, n, s.d)) return RA_ERR_INVALID_ARG;
+  return RA_OK;
+}
+
+bool same_rows(const ra_rows& a, const ra_rows& b) {
+  return a.stride_b == b.stride_b && a.stride_h == b.stride_h && a.stride_n == b.stride_n;
+}
+
+// Can every row of r be moved in 16-byte vectors?
+bool vectors_fit(const ra_rows& r, int V, size_t elem) {
+  return aligned_to(r.ptr, 16) && r.stride_b % V == 0 && r.stride_h % V == 0 &&
+         r.stride_n % V == 0 && V * elem == 16;
+}
+
+template <typename T, int V, bool HALF, bool BWD>
+cudaError_t launch_rot(const RotArgs& a, dim3 grid, cudaStream_t s) {
+  constexpr int NP = HALF ? V : (V > 1 ? V / 2 : 1);
+  const size_t smem =
+      BWD && a.part ? sizeof(double) * (size_t)a.rot_units * NP * (size_t)a.tile : 0;
+  rotary_kernel<T, V, HALF, BWD><<<grid, kThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, bool BWD>
+cudaError_t launch_rot_t(const RotArgs& a, bool vec, bool half, dim3 grid, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  if (vec)
+    return half ? launch_rot<T, V, true, BWD>(a, grid, s)
+                : launch_rot<T, V, false, BWD>(a, grid, s);
+  return half ? launch_rot<T, 1, true, BWD>(a, grid, s) : launch_rot<T, 1, false, BWD>(a, grid, s);
+}
+
+// Shared by both directions.  part: fp64 partial torques (backward with dalpha), else null.
+ra_status run(const ra_rotary* r, int64_t B, int64_t n, int32_t dtype, const double* freqs,
+              const int32_t* pos, const ra_rows* in[2], const ra_rows* out[2],
+              const ra_rows* x[2], double* part, int* parts, bool bwd, int kid,
+              cudaStream_t s) {
+  RotArgs a{};
+  const size_t elem = elem_bytes(dtype);
+  int V = (int)(16 / elem);
+  const bool half = r->layout == RA_HALF;
+  bool vec = r->d % V == 0 && r->rot_dim % V == 0 && (!half || (r->rot_dim / 2) % V == 0);
+  int64_t heads = 0;
+  for (int z = 0; z < 2; ++z) {
+    if (!in[z]) continue;
+    HeadRows& t = a.t[z];
+    t.in = in[z]->ptr, t.out = out[z]->ptr, t.H = (int)in[z]->H;
+    t.ib = in[z]->stride_b, t.ih = in[z]->stride_h, t.in_ = in[z]->stride_n;
+    t.ob = out[z]->stride_b, t.oh = out[z]->stride_h, t.on = out[z]->stride_n;
+    vec = vec && vectors_fit(*in[z], V, elem) && vectors_fit(*out[z], V, elem);
+    if (part) {
+      t.x = x[z]->ptr;
+      t.xb = x[z]->stride_b, t.xh = x[z]->stride_h, t.xn = x[z]->stride_n;
+      vec = vec && vectors_fit(*x[z], V, elem);
+    }
+    heads += t.H;
+  }
+  if (!vec) V = 1;
+  a.pos = pos, a.freqs = freqs, a.amplitude = r->amplitude, a.part = part;
+  a.tokens = B * n, a.n = (int)n, a.r = (int)r->rot_dim, a.d = (int)r->d;
+  a.rot_units = half ? a.r / 2 / V : a.r / (V > 1 ? V : 2);
+  a.units = a.rot_units + (a.d - a.r) / V;
+  a.tile = kThreads / a.units;  // d <= 256: at least one token
+  const long long tiles = (a.tokens + a.tile - 1) / a.tile;
+  // Few tokens: the heads are split over the blocks' second dimension, at least kUnroll heads
+  // each, until there are about eight blocks per SM (the angles are then formed once per
+  // chunk, which idle SMs do for nothing).
+  const long long want = (kRotaryBlocks + tiles - 1) / tiles;
+  const int64_t chunks = std::max<int64_t>(
+      1, std::min<int64_t>(want, (heads + kUnroll - 1) / kUnroll));
+  a.heads_per_chunk = (int)((heads + chunks - 1) / chunks);
+  const unsigned gy = (unsigned)((heads + a.heads_per_chunk - 1) / a.heads_per_chunk);
+  long long gx = tiles;
+  if (part) gx = std::min<long long>(gx, std::max<long long>(1, kRotaryParts / gy));
+  if (gx > 0x7fffffff) return RA_ERR_UNSUPPORTED;
+  if (parts) *parts = (int)(gx * gy);
+  const dim3 grid((unsigned)gx, gy);
+  cudaError_t e;
+  {
+    const TimingScope timed(kid, s);
+    if (dtype == RA_BF16)
+      e = bwd ? launch_rot_t<__nv_bfloat16, true>(a, vec, half, grid, s)
+              : launch_rot_t<__nv_bfloat16, false>(a, vec, half, grid, s);
+    else
+      e = bwd ? launch_rot_t<float, true>(a, vec, half, grid, s)
+              : launch_rot_t<float, false>(a, vec, half, grid, s);
+  }
+  return e == cudaSuccess ? RA_OK : RA_ERR_CUDA;
+}
+
+ra_status check_call(const ra_rotary* r, int64_t B, int64_t n, int32_t dtype, const void* freqs,
+                     const void* pos) {
+  const ra_status st = check_rotary(r);
+  if (st != RA_OK) return st;
+  if (dtype != RA_F32 && dtype != RA_BF16) return RA_ERR_INVALID_ARG;
+  if (B < 1 || n < 1) return RA_ERR_INVALID_ARG;
+  if (B > (int64_t(1) << 30) || n > (int64_t(1) << 30) || B * n > (int64_t(1) << 30))
+    return RA_ERR_UNSUPPORTED;
+  if (!freqs || !aligned_to(freqs, 8) || !aligned_to(pos, 4)) return RA_ERR_INVALID_ARG;
+  return RA_OK;
+}
+
+}  // namespace
+
+ra_status check_rotary(const ra_rotary* r) {
+  if (!r) return RA_ERR_INVALID_ARG;
+  if (r->d < 2 || r->d % 2 || r->rot_dim < 2 || r->rot_dim % 2 || r->rot_dim > r->d)
+    return RA_ERR_INVALID_ARG;
+  if (r->d > 256) return RA_ERR_UNSUPPORTED;
+  if (!(r->base > 0.0) || !std::isfinite(r->base)) return RA_ERR_INVALID_ARG;
+  if (r->layout != RA_INTERLEAVED && r->layout != RA_HALF) return RA_ERR_INVALID_ARG;
+  if (r->scaling < RA_SCALE_NONE || r->scaling > RA_SCALE_PARTS) return RA_ERR_INVALID_ARG;
+  if (r->scaling != RA_SCALE_NONE && (!(r->factor > 0.0) || !std::isfinite(r->factor)))
+    return RA_ERR_INVALID_ARG;
+  if (r->scaling == RA_SCALE_PARTS &&
+      (!(r->orig_len > 0.0) || !std::isfinite(r->orig_len) || !(r->fast > r->slow) ||
+       !std::isfinite(r->fast) || !std::isfinite(r->slow)))
+    return RA_ERR_INVALID_ARG;
+  if (!std::isfinite(r->amplitude)) return RA_ERR_INVALID_ARG;
+  if (r->fixed_bands < 0 || r->fixed_bands > r->rot_dim / 2 || r->reserved != 0)
+    return RA_ERR_INVALID_ARG;
+  return RA_OK;
+}
+
+}  // namespace ra
+
+using namespace ra;
+
+extern "C" {
+
+ra_status rope_attn_rotary_freqs(const ra_rotary* r, const float* alpha, double* freqs,
+                                 void* stream) {
+  const ra_status st = check_rotary(r);
+  if (st != RA_OK) return st;
+  if (!freqs || !aligned_to(freqs, 8) || !aligned_to(alpha, 4)) return RA_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const TimingScope timed(K_ROTARY_FREQS, s);
+  rotary_freqs_kernel<<<(unsigned)((r->rot_dim / 2 + 31) / 32), 32, 0, s>>>(*r, alpha, freqs);
+  return cudaGetLastError() == cudaSuccess ? RA_OK : RA_ERR_CUDA;
+}
+
+ra_status rope_attn_rotary(const ra_rotary* r, int64_t B, int64_t n, int32_t dtype,
+                           const double* freqs, const int32_t* pos, const ra_rows* q,
+                           const ra_rows* q_out, const ra_rows* k, const ra_rows* k_out,
+                           void* stream) {
+  ra_status st = check_call(r, B, n, dtype, freqs, pos);
+  if (st != RA_OK) return st;
+  if ((k == nullptr) != (k_out == nullptr)) return RA_ERR_INVALID_ARG;
+  const ra_rows* in[2] = {q, k};
+  const ra_rows* out[2] = {q_out, k_out};
+  const ra_rows* none[2] = {nullptr, nullptr};
+  for (int z = 0; z < 2; ++z) {
+    if (z == 1 && !k) continue;
+    if ((st = check_rows(in[z], *r, B, n, dtype, false)) != RA_OK) return st;
+    if ((st = check_rows(out[z], *r, B, n, dtype, true)) != RA_OK) return st;
+    if (in[z]->H != out[z]->H) return RA_ERR_INVALID_ARG;
+    if (in[z]->ptr == out[z]->ptr && !same_rows(*in[z], *out[z])) return RA_ERR_INVALID_ARG;
+  }
+  return run(r, B, n, dtype, freqs, pos, in, out, none, nullptr, nullptr, false, K_ROTARY,
+             static_cast<cudaStream_t>(stream));
+}
+
+size_t rope_attn_rotary_workspace_bytes(const ra_rotary* r) {
+  if (check_rotary(r) != RA_OK) return 0;
+  return align_up(sizeof(double) * (size_t)kRotaryParts * (size_t)(r->rot_dim / 2), 1024);
+}
+
+ra_status rope_attn_rotary_bwd(const ra_rotary* r, int64_t B, int64_t n, int32_t dtype,
+                               const double* freqs, const int32_t* pos, const ra_rows* dq_rot,
+                               const ra_rows* dq, const ra_rows* dk_rot, const ra_rows* dk,
+                               const ra_rows* q, const ra_rows* k, float* dalpha, void* ws,
+                               size_t ws_bytes, void* stream) {
+  ra_status st = check_call(r, B, n, dtype, freqs, pos);
+  if (st != RA_OK) return st;
+  if ((dk_rot == nullptr) != (dk == nullptr)) return RA_ERR_INVALID_ARG;
+  const ra_rows* in[2] = {dq_rot, dk_rot};
+  const ra_rows* out[2] = {dq, dk};
+  const ra_rows* x[2] = {q, k};
+  for (int z = 0; z < 2; ++z) {
+    if (z == 1 && !dk) continue;
+    if ((st = check_rows(in[z], *r, B, n, dtype, false)) != RA_OK) return st;
+    if ((st = check_rows(out[z], *r, B, n, dtype, true)) != RA_OK) return st;
+    if (in[z]->H != out[z]->H) return RA_ERR_INVALID_ARG;
+    if (in[z]->ptr == out[z]->ptr && !same_rows(*in[z], *out[z])) return RA_ERR_INVALID_ARG;
+    if (dalpha) {
+      if ((st = check_rows(x[z], *r, B, n, dtype, false)) != RA_OK) return st;
+      if (x[z]->H != in[z]->H || x[z]->ptr == out[z]->ptr) return RA_ERR_INVALID_ARG;
+    }
+  }
+  double* part = nullptr;
+  if (dalpha) {
+    if (!aligned_to(dalpha, 4)) return RA_ERR_INVALID_ARG;
+    if (!ws || !aligned_to(ws, 256) || ws_bytes < rope_attn_rotary_workspace_bytes(r))
+      return RA_ERR_WORKSPACE;
+    part = static_cast<double*>(ws);
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int parts = 0;
+  st = run(r, B, n, dtype, freqs, pos, in, out, x, part, &parts, true, K_ROTARY_BWD, s);
+  if (st != RA_OK || !dalpha) return st;
+  const int M = (int)(r->rot_dim / 2);
+  const TimingScope timed(K_ROTARY_DALPHA, s);
+  rotary_dalpha_kernel<<<(unsigned)M, 128, 0, s>>>(part, parts, M, freqs, dalpha);
+  return cudaGetLastError() == cudaSuccess ? RA_OK : RA_ERR_CUDA;
+}
+
+}  // extern "C"

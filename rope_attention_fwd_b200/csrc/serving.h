@@ -1,0 +1,212 @@
+// serving.h -- shared by the rotation and the paged-cache calls: argument checks, the cache's
+// layout, and how the attention over it is cut into pieces of work.  The arithmetic is plain
+// host/device code, so that the host tests run it too.
+#pragma once
+#include <algorithm>
+#include <cstddef>
+#include <cstdint>
+
+#include "common.h"
+
+namespace ra {
+
+// ------------------------------------------------------------------ rotation
+constexpr int kRotaryBlocks = 1184;  // blocks wanted: 8 per SM
+constexpr int kRotaryParts = 592;    // most partial torques of a backward
+constexpr int64_t kMaxHeads = 65536;
+
+inline size_t elem_bytes(int32_t dtype) { return dtype == RA_BF16 ? 2 : 4; }
+ra_status check_rotary(const ra_rotary* r);
+
+// ------------------------------------------------------------------ cache layout
+constexpr int kGroup = 64;      // channels of a (step, lo) pair
+constexpr int kBlock = 16;      // tokens of a block
+
+__host__ __device__ constexpr int code_bytes(int d) { return kBlock * d / 2; }
+__host__ __device__ constexpr int pair_bytes(int d) { return kBlock * (d / kGroup) * 4; }
+// Bytes of one block: K codes, K pairs, V codes, V pairs.
+__host__ __device__ constexpr int block_bytes(int d) { return 2 * (code_bytes(d) + pair_bytes(d)); }
+__host__ __device__ constexpr int value_offset(int d) { return code_bytes(d) + pair_bytes(d); }
+
+struct CacheDims {
+  int B, T, Hq, Hkv, d;
+  int pages, page_blocks, max_pages;  // page_blocks: 16-token blocks of a page
+  int max_q, window, causal;
+  float scale;
+};
+
+// Byte offset of block `blk` of page `page` for one kv head.
+__host__ __device__ inline size_t block_at(const CacheDims& c, int page, int h, int blk) {
+  return (((size_t)page * (size_t)c.Hkv + (size_t)h) * (size_t)c.page_blocks + (size_t)blk) *
+         (size_t)block_bytes(c.d);
+}
+
+// May page number `page` (as a table holds it) be followed?
+__host__ __device__ inline bool page_ok(const CacheDims& c, int page) {
+  return (unsigned)page < (unsigned)c.pages;
+}
+
+// What is wrong with a sequence that has rows q0 .. q1 - 1 and L cached tokens (0: nothing).
+__host__ __device__ inline int sequence_fault(const CacheDims& c, int q0, int q1, int L) {
+  if (q0 < 0 || q1 < q0 || q1 > c.T || q1 - q0 > c.max_q) return RA_CACHE_BAD_INDPTR;
+  if (L < 0 || (long long)L > (long long)c.max_pages * c.page_blocks * kBlock)
+    return RA_CACHE_BAD_LENGTH;
+  return 0;
+}
+
+// ------------------------------------------------------------------ pieces of attention work
+// The rows of a sequence that share a kv head are its tokens times the G = Hq / Hkv query
+// heads (row = token * G + head of the group), cut into tiles of `tile` rows.  An item is one
+// (sequence, kv head, row tile); its keys are walked in steps of kStep tokens.  All items'
+// steps are numbered through (sequences, then heads, then row tiles, then steps) and dealt out
+// in equal runs of `per` steps to the blocks of a launch of fixed size, whatever the lengths:
+// long caches split over many blocks, short ones share one, and a captured launch keeps its
+// balance when the lengths change.  An item that lies in several runs is joined by the combine
+// kernel from fp32 partial sums.
+constexpr int kStep = 128;
+
+struct SeqWork {
+  int q0, qn, L;     // first row in the batch, tokens, cached tokens
+  int first;         // first key of the first step (a multiple of kBlock)
+  int steps;         // steps of an item (0: no item)
+  int tiles;         // row tiles
+  long long total;   // steps of the sequence over all heads and tiles
+};
+
+// The steps of sequence (q0, q1, L) for a kernel that takes sequences of min_rows < rows <=
+// max_rows; none if the sequence is faulty, empty or another kernel's.
+__host__ __device__ inline SeqWork seq_work(const CacheDims& c, int q0, int q1, int L, int tile,
+                                            long long min_rows, long long max_rows) {
+  SeqWork w{q0, 0, L, 0, 0, 0, 0};
+  if (sequence_fault(c, q0, q1, L) || q1 == q0) return w;
+  const long long rows = (long long)(q1 - q0) * (c.Hq / c.Hkv);
+  if (rows <= min_rows || rows > max_rows) return w;
+  w.qn = q1 - q0;
+  int begin = 0;
+  if (c.causal && c.window > 0) {  // the first token's window
+    const long long b = (long long)L - w.qn - c.window + 1;
+    begin = b > 0 ? (int)(b < L ? b : L) : 0;
+  }
+  w.first = begin / kBlock * kBlock;
+  w.steps = (L - w.first + kStep - 1) / kStep;
+  if (w.steps < 1) w.steps = 1;  // no key: one empty step writes the rows
+  w.tiles = (int)((rows + tile - 1) / tile);
+  w.total = (long long)c.Hkv * w.tiles * w.steps;
+  return w;
+}
+
+// Steps per block: all of them dealt evenly to at most `blocks` blocks, at least min_steps each.
+__host__ __device__ inline long long steps_per_block(long long total, int blocks, int min_steps) {
+  const long long per = (total + blocks - 1) / blocks;
+  return per < min_steps ? min_steps : per;
+}
+
+// A block's run of steps and where it begins.
+struct Run {
+  long long begin, end, per;  // steps [begin, end) of the launch's total
+  int b;                      // the sequence of `begin`
+  long long base;             // the total's number of that sequence's first step
+};
+
+// One item's share of a block's run.
+struct Segment {
+  int b, h, tile;
+  int s0, s1;            // its steps [s0, s1) of w.steps
+  bool first, last;      // holds the item's first / last step
+  int followers;         // first and not last: blocks after this one that go on with it
+  SeqWork w;
+};
+
+// Walks the segments of a run in order; next() is uniform over the block.
+template <typename F>
+struct Walk {
+  long long at, end, base, per;
+  int b, B;
+  SeqWork w;
+  F work;  // sequence number -> SeqWork
+
+  __host__ __device__ Walk(const F& f, const Run& r, int sequences)
+      : at(r.begin), end(r.end), base(r.base), per(r.per), b(r.b), B(sequences), work(f) {
+    if (at < end) w = work(b);
+  }
+  __host__ __device__ bool next(Segment& s) {
+    if (at >= end) return false;
+    while (at >= base + w.total) {  // at < end <= total: a later sequence holds it
+      base += w.total;
+      if (++b >= B) return false;
+      w = work(b);
+    }
+    const long long rel = at - base;
+    const long long item = rel / w.steps;
+    s.b = b;
+    s.h = (int)(item / w.tiles);
+    s.tile = (int)(item - (long long)s.h * w.tiles);
+    s.s0 = (int)(rel - item * w.steps);
+    const long long left = end - at;
+    s.s1 = left < w.steps - s.s0 ? s.s0 + (int)left : w.steps;
+    s.first = s.s0 == 0;
+    s.last = s.s1 == w.steps;
+    s.followers = 0;
+    if (s.first && !s.last) {
+      const long long item_end = base + (item + 1) * w.steps;
+      s.followers = (int)((item_end - 1) / per - at / per);
+    }
+    s.w = w;
+    at += s.s1 - s.s0;
+    return true;
+  }
+};
+
+// Keys that row `row` (of a sequence's rows of one kv head) sees: lo .. hi - 1.
+struct KeyRange {
+  int lo, hi;
+};
+__host__ __device__ inline KeyRange row_keys(const CacheDims& c, const SeqWork& w, long long row,
+                                             int G) {
+  KeyRange r{0, w.L};
+  if (c.causal) {
+    const long long pos = (long long)w.L - w.qn + row / G;
+    r.hi = pos < 0 ? 0 : (int)(pos + 1);
+    if (c.window > 0 && pos - c.window + 1 > 0) r.lo = (int)(pos - c.window + 1);
+    if (r.lo > r.hi) r.lo = r.hi;
+  }
+  return r;
+}
+
+// ------------------------------------------------------------------ attention workspace
+// [error word | one descriptor per block | per block two partial results: m and l, then the
+// weighted sums of every row of a tile].  Partial 2c is block c's first item when the item
+// began in an earlier block, 2c + 1 its last item when the item goes on in later blocks.
+constexpr size_t kCacheErrBytes = 1024;
+constexpr int kRowsBlocks = 592;   // launch of the kernels for a few rows: 4 per SM
+constexpr int kRowsTile = 16;      // most rows of their tiles
+constexpr int kChunkBlocks = 148;  // launch of the chunk kernel: 1 per SM
+constexpr int kChunkTile = 256;    // rows of its tiles
+constexpr int kChunkMinRows = 64;  // the chunk kernel takes sequences of more rows than this
+
+struct PartDesc {      // the split item that begins in a block: the blocks after it that go on
+  int followers;       // 0: no such item
+  int b, h, tile;
+};
+
+struct CacheWs {
+  size_t desc, ml, acc, total;
+};
+#ifdef __CUDACC__
+ra_status check_cache(const ra_cache* p);
+CacheDims cache_dims(const ra_cache& p);
+ra_status check_cache_call(const ra_cache* p, const void* cache, const int32_t* table,
+                           const int32_t* indptr, const int32_t* kv_len, void* ws,
+                           size_t ws_bytes);
+#endif
+
+inline CacheWs cache_ws(int blocks, int tile, int d) {
+  CacheWs w{};
+  w.desc = kCacheErrBytes;
+  w.ml = align_up(w.desc + sizeof(PartDesc) * (size_t)blocks, 1024);
+  w.acc = align_up(w.ml + sizeof(float) * 2 * 2 * (size_t)blocks * tile, 1024);
+  w.total = align_up(w.acc + sizeof(float) * 2 * (size_t)blocks * tile * d, 1024);
+  return w;
+}
+
+}  // namespace ra
