@@ -28,7 +28,7 @@ namespace {
 // lo + step * code is rounded once.
 constexpr int kF32Threads = 128;
 
-template <typename T, int D, int R>
+template <int D, int R>
 __global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const AttnArgs a) {
   constexpr int DL = D / 32;  // channels of a lane in the value product
   __shared__ __align__(16) float q_s[R][D];
@@ -53,13 +53,9 @@ __global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const AttnA
       float x = 0.f;
       if (r < rows) {
         const long long row = row0 + r;
-        const T* src = static_cast<const T*>(a.q) + (s.w.q0 + row / G) * a.q_n +
+        const float* src = static_cast<const float*>(a.q) + (s.w.q0 + row / G) * a.q_n +
                        ((long long)s.h * G + row % G) * a.q_h;
-        Vec<T, 1> v;
-        float f[1];
-        v.load(src + ch);
-        v.get(f);
-        x = f[0] * scale_log2;
+        x = src[ch] * scale_log2;
       }
       q_s[r][ch] = x;
     }
@@ -207,10 +203,7 @@ __global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const AttnA
       if (whole) {
         const long long row = row0 + r;
         const long long at = (s.w.q0 + row / G) * c.Hq + (long long)s.h * G + row % G;
-        Vec<T, 1> v;
-        const float f[1] = {wl > 0.f ? sum / wl : 0.f};
-        v.set(f);
-        v.store(static_cast<T*>(a.o) + at * D + ch);
+        static_cast<float*>(a.o)[at * D + ch] = wl > 0.f ? sum / wl : 0.f;
         if (ch == 0) a.lse[at] = (mx + log2f(wl)) * 0.6931471805599453f;
       } else {
         a.acc[(slot * a.tile + r) * D + ch] = sum;
@@ -294,21 +287,21 @@ __global__ void __launch_bounds__(kCombineThreads) cache_combine_kernel(const At
   }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_f32(AttnArgs& a, int rows, cudaStream_t s) {
   // the smallest tile that holds the rows of the longest sequence
   if (rows <= 1) {
     a.tile = 1;
-    cache_attn_f32_kernel<T, D, 1><<<kRowsBlocks, kF32Threads, 0, s>>>(a);
+    cache_attn_f32_kernel<D, 1><<<kRowsBlocks, kF32Threads, 0, s>>>(a);
   } else if (rows <= 2) {
     a.tile = 2;
-    cache_attn_f32_kernel<T, D, 2><<<kRowsBlocks, kF32Threads, 0, s>>>(a);
+    cache_attn_f32_kernel<D, 2><<<kRowsBlocks, kF32Threads, 0, s>>>(a);
   } else if (rows <= 4) {
     a.tile = 4;
-    cache_attn_f32_kernel<T, D, 4><<<kRowsBlocks, kF32Threads, 0, s>>>(a);
+    cache_attn_f32_kernel<D, 4><<<kRowsBlocks, kF32Threads, 0, s>>>(a);
   } else {
     a.tile = 8;
-    cache_attn_f32_kernel<T, D, 8><<<kRowsBlocks, kF32Threads, 0, s>>>(a);
+    cache_attn_f32_kernel<D, 8><<<kRowsBlocks, kF32Threads, 0, s>>>(a);
   }
   return cudaGetLastError();
 }
@@ -377,19 +370,19 @@ ra_status rope_attn_cache_attn(const ra_cache* p, const void* cache, const int32
   a.acc = reinterpret_cast<float*>(base + w.acc);
   a.min_rows = 0, a.max_rows = int64_t(1) << 62;
   a.min_steps = 2;
-  const int rows = (int)std::min<int64_t>(most_rows, 8);
   cudaError_t e;
-  {
+  int blocks = kRowsBlocks;
+  if (p->dtype == RA_BF16) {
+    const TimingScope timed(K_CACHE_ATTN, s);
+    e = launch_cache_rows(a, most_rows, &blocks, s);
+  } else {
     const TimingScope timed(K_CACHE_ATTN_F32, s);
-    if (p->dtype == RA_BF16)
-      e = p->d == 64 ? launch_f32<__nv_bfloat16, 64>(a, rows, s)
-                     : launch_f32<__nv_bfloat16, 128>(a, rows, s);
-    else
-      e = p->d == 64 ? launch_f32<float, 64>(a, rows, s) : launch_f32<float, 128>(a, rows, s);
+    const int rows = (int)std::min<int64_t>(most_rows, 8);
+    e = p->d == 64 ? launch_f32<64>(a, rows, s) : launch_f32<128>(a, rows, s);
   }
   if (e != cudaSuccess) return RA_ERR_CUDA;
   const TimingScope timed(K_CACHE_COMBINE, s);
-  e = launch_cache_combine(a, kRowsBlocks, p->dtype, (int)std::min<int64_t>(most_rows, a.tile), s);
+  e = launch_cache_combine(a, blocks, p->dtype, (int)std::min<int64_t>(most_rows, a.tile), s);
   return e == cudaSuccess ? RA_OK : RA_ERR_CUDA;
 }
 

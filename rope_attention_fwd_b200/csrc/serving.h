@@ -178,9 +178,10 @@ __host__ __device__ inline KeyRange row_keys(const CacheDims& c, const SeqWork& 
 // weighted sums of every row of a tile].  Partial 2c is block c's first item when the item
 // began in an earlier block, 2c + 1 its last item when the item goes on in later blocks.
 constexpr size_t kCacheErrBytes = 1024;
-constexpr int kRowsBlocks = 592;   // launch of the kernels for a few rows: 4 per SM
+constexpr int kSms = 148;
+constexpr int kRowsBlocks = 4 * kSms;  // largest launch of the kernels for a few rows
 constexpr int kRowsTile = 16;      // most rows of their tiles
-constexpr int kChunkBlocks = 148;  // launch of the chunk kernel: 1 per SM
+constexpr int kChunkBlocks = kSms;  // launch of the chunk kernel: 1 per SM
 constexpr int kChunkTile = 256;    // rows of its tiles
 constexpr int kChunkMinRows = 64;  // the chunk kernel takes sequences of more rows than this
 
