@@ -381,43 +381,53 @@ def rope_attn_alpha_adam(alpha, dalpha, m1, m2, step, lr, beta1=0.9, beta2=0.999
 
 
 # ---------------------------------------------------------------- rotation, paged cache
+# A decode step makes several of these calls per layer on little work, so the checks go by the
+# cheapest attributes (get_device, dtype, shape) and build nothing unless they fail.
 def _serving_device(fn, t):
-    """The CUDA device of t (the calls below take device memory only)."""
-    if t.device.type != "cuda":
+    """The index of t's CUDA device (the calls below take device memory only)."""
+    if not t.is_cuda:
         raise ValueError(f"{fn}: tensors must be on a CUDA device, got {t.device}")
-    return t.device
+    return t.get_device()
 
 
-def _call(fn, device, *args):
-    """fn(*args, stream) with the tensors' device current (kernels launch on it)."""
-    if torch.cuda.current_device() == device.index:
-        code = getattr(lib(), fn)(*args, _stream(device))
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):   # the same handle without its wrapper
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _call(fn, index, *args):
+    """fn(*args, stream) with device `index` current (kernels launch on it)."""
+    if torch.cuda.current_device() == index:
+        code = getattr(lib(), fn)(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            code = getattr(lib(), fn)(*args, _stream(device))
+        with torch.cuda.device(index):
+            code = getattr(lib(), fn)(*args, _raw_stream(index))
     if code != 0:
         raise RopeAttnError(fn, code)
 
 
-def _vector(fn, name, t, device, dtype, shape):
-    """A contiguous tensor of the given type and shape on `device`."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or \
-            not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape "
-                         f"{tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} "
-                         f"(strides {t.stride()}) on {t.device}")
+def _vector(fn, name, t, index, dtype, shape):
+    """The address of a contiguous tensor of the given type and shape on device `index`."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
+        return t.data_ptr()
+    raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
+                     f"on device {index}, got {t.dtype} {tuple(t.shape)} (strides {t.stride()}) "
+                     f"on {t.device}")
 
 
-def _head_rows(fn, name, t, device, dtype, shape):
+def _head_rows(fn, name, t, index, dtype, shape):
     """RaRows of [B, H, n, d] (4 dimensions) or [T, H, d] (3): any strides, channels
     contiguous."""
-    if t.dtype != dtype or t.device != device or t.shape != shape:
-        raise ValueError(f"{fn}: {name} must be {dtype} of shape {tuple(shape)} on {device}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        raise ValueError(f"{fn}: {name} must be {dtype} of shape {tuple(shape)} on device {index}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{fn}: {name} must have contiguous channels, got strides {st}")
-    if len(shape) == 4:
+    if len(st) == 4:
         return RaRows(t.data_ptr(), shape[1], st[0], st[1], st[2])
     return RaRows(t.data_ptr(), shape[1], 0, st[1], st[0])
 
@@ -447,16 +457,13 @@ def rope_attn_rotary_freqs(spec, alpha=None, freqs=None, device=None):
     computed anew whenever alpha changes."""
     fn = "rope_attn_rotary_freqs"
     half = spec.rot_dim // 2
-    ref = alpha if alpha is not None else freqs
-    if ref is None:
-        ref = freqs = torch.empty(half, dtype=torch.float64, device=device or "cuda")
-    dev = _serving_device(fn, ref)
-    if alpha is not None:
-        _vector(fn, "alpha", alpha, dev, torch.float32, (half,))
     if freqs is None:
-        freqs = torch.empty(half, dtype=torch.float64, device=dev)
-    _vector(fn, "freqs", freqs, dev, torch.float64, (half,))
-    _call(fn, dev, ctypes.byref(spec), _ptr(alpha), _ptr(freqs))
+        freqs = torch.empty(half, dtype=torch.float64,
+                            device=alpha.device if alpha is not None else device or "cuda")
+    dev = _serving_device(fn, freqs)
+    _call(fn, dev, ctypes.byref(spec),
+          None if alpha is None else _vector(fn, "alpha", alpha, dev, torch.float32, (half,)),
+          _vector(fn, "freqs", freqs, dev, torch.float64, (half,)))
     return freqs
 
 
@@ -466,10 +473,9 @@ def _rotary_args(fn, spec, freqs, x, pos):
                          f"{x.dtype} {tuple(x.shape)}")
     dev = _serving_device(fn, x)
     B, _, n, _ = x.shape
-    _vector(fn, "freqs", freqs, dev, torch.float64, (spec.rot_dim // 2,))
-    if pos is not None:
-        _vector(fn, "pos", pos, dev, torch.int32, (B, n))
-    return dev, B, n
+    f = _vector(fn, "freqs", freqs, dev, torch.float64, (spec.rot_dim // 2,))
+    p = None if pos is None else _vector(fn, "pos", pos, dev, torch.int32, (B, n))
+    return dev, (ctypes.byref(spec), B, n, _DTYPE[x.dtype], f, p)
 
 
 def _same_tokens(fn, name, t, x):
@@ -482,7 +488,7 @@ def rope_attn_rotary(spec, freqs, q, k=None, pos=None, q_out=None, k_out=None):
     """(q~, k~): q [B, Hq, n, d] and k [B, Hk, n, d] (any strides, channels contiguous; k may be
     None) rotated at positions pos (int32 [B, n]; None: 0..n-1).  q_out may be q, k_out k."""
     fn = "rope_attn_rotary"
-    dev, B, n = _rotary_args(fn, spec, freqs, q, pos)
+    dev, head = _rotary_args(fn, spec, freqs, q, pos)
     q_out = torch.empty_like(q) if q_out is None else q_out
     rows = [_head_rows(fn, "q", q, dev, q.dtype, q.shape),
             _head_rows(fn, "q_out", q_out, dev, q.dtype, q.shape), None, None]
@@ -491,8 +497,7 @@ def rope_attn_rotary(spec, freqs, q, k=None, pos=None, q_out=None, k_out=None):
         k_out = torch.empty_like(k) if k_out is None else k_out
         rows[2] = _head_rows(fn, "k", k, dev, q.dtype, k.shape)
         rows[3] = _head_rows(fn, "k_out", k_out, dev, q.dtype, k.shape)
-    _call(fn, dev, ctypes.byref(spec), B, n, _DTYPE[q.dtype], _ptr(freqs), _ptr(pos),
-          *[_opt(r) for r in rows])
+    _call(fn, dev, *head, *[_opt(r) for r in rows])
     return q_out, k_out if k is not None else None
 
 
@@ -505,7 +510,7 @@ def rope_attn_rotary_bwd(spec, freqs, dq_rot, dk_rot=None, q=None, k=None, pos=N
     """(dq, dk, dalpha) from the gradients dq_rot, dk_rot of the rotated tensors.  q and k (the
     forward's inputs) are needed for dalpha only; frozen_alpha: None is returned in its place."""
     fn = "rope_attn_rotary_bwd"
-    dev, B, n = _rotary_args(fn, spec, freqs, dq_rot, pos)
+    dev, head = _rotary_args(fn, spec, freqs, dq_rot, pos)
     dt = dq_rot.dtype
     dq = torch.empty_like(dq_rot) if dq is None else dq
     rows = [_head_rows(fn, "dq_rot", dq_rot, dev, dt, dq_rot.shape),
@@ -515,8 +520,9 @@ def rope_attn_rotary_bwd(spec, freqs, dq_rot, dk_rot=None, q=None, k=None, pos=N
         dk = torch.empty_like(dk_rot) if dk is None else dk
         rows[2] = _head_rows(fn, "dk_rot", dk_rot, dev, dt, dk_rot.shape)
         rows[3] = _head_rows(fn, "dk", dk, dev, dt, dk_rot.shape)
+    out, w, nbytes = None, None, 0
     if frozen_alpha:
-        dalpha = ws = None
+        dalpha = None
     else:
         if q is None or (k is None) != (dk_rot is None):
             raise ValueError(f"{fn}: dalpha needs the forward's q (and k, if it had one); pass "
@@ -526,14 +532,14 @@ def rope_attn_rotary_bwd(spec, freqs, dq_rot, dk_rot=None, q=None, k=None, pos=N
             rows[5] = _head_rows(fn, "k", k, dev, dt, dk_rot.shape)
         half = spec.rot_dim // 2
         if dalpha is None:
-            dalpha = torch.empty(half, dtype=torch.float32, device=dev)
-        _vector(fn, "dalpha", dalpha, dev, torch.float32, (half,))
+            dalpha = torch.empty(half, dtype=torch.float32, device=dq.device)
+        out = _vector(fn, "dalpha", dalpha, dev, torch.float32, (half,))
         if ws is None:
             ws = torch.empty(rope_attn_rotary_workspace_bytes(spec), dtype=torch.uint8,
-                             device=dev)
-        _vector(fn, "ws", ws, dev, torch.uint8, (ws.numel(),))
-    _call(fn, dev, ctypes.byref(spec), B, n, _DTYPE[dt], _ptr(freqs), _ptr(pos),
-          *[_opt(r) for r in rows], _ptr(dalpha), _ptr(ws), ws.numel() if ws is not None else 0)
+                             device=dq.device)
+        nbytes = ws.numel()
+        w = _vector(fn, "ws", ws, dev, torch.uint8, (nbytes,))
+    _call(fn, dev, *head, *[_opt(r) for r in rows], out, w, nbytes)
     return dq, dk if dk_rot is not None else None, dalpha
 
 
@@ -582,19 +588,22 @@ _CACHE_DTYPE = {RA_F32: torch.float32, RA_BF16: torch.bfloat16}
 
 
 def _cache_args(fn, plan, cache, table, indptr, kv_len, ws):
+    """(device index, leading arguments of the C call, ws and its size, dtype)."""
     dev = _serving_device(fn, cache)
-    if cache.dtype != torch.uint8 or not cache.is_contiguous() or \
-            cache.numel() != rope_attn_cache_bytes(plan):
-        raise ValueError(f"{fn}: cache must be a contiguous uint8 tensor of "
-                         f"{rope_attn_cache_bytes(plan)} bytes, got {cache.dtype} "
-                         f"{tuple(cache.shape)} (strides {cache.stride()})")
-    _vector(fn, "table", table, dev, torch.int32, (plan.B, plan.max_pages))
-    _vector(fn, "indptr", indptr, dev, torch.int32, (plan.B + 1,))
-    _vector(fn, "kv_len", kv_len, dev, torch.int32, (plan.B,))
+    B, d = plan.B, plan.d
+    # pages x heads x blocks of 16 tokens, each 32 (d / 2 + 4 d / 64) bytes
+    want = plan.pages * plan.Hkv * (plan.page_size // 16) * (18 * d)
+    if cache.dtype is not torch.uint8 or not cache.is_contiguous() or cache.numel() != want:
+        raise ValueError(f"{fn}: cache must be a contiguous uint8 tensor of {want} bytes, got "
+                         f"{cache.dtype} {tuple(cache.shape)} (strides {cache.stride()})")
     if ws is None:
-        ws = cache_workspace(plan, dev)
-    _vector(fn, "ws", ws, dev, torch.uint8, (ws.numel(),))
-    return dev, ws, (ctypes.byref(plan), _ptr(cache), _ptr(table), _ptr(indptr), _ptr(kv_len))
+        ws = cache_workspace(plan, cache.device)
+    n = ws.numel()
+    return dev, (ctypes.byref(plan), cache.data_ptr(),
+                 _vector(fn, "table", table, dev, torch.int32, (B, plan.max_pages)),
+                 _vector(fn, "indptr", indptr, dev, torch.int32, (B + 1,)),
+                 _vector(fn, "kv_len", kv_len, dev, torch.int32, (B,))), \
+        (_vector(fn, "ws", ws, dev, torch.uint8, (n,)), n), _CACHE_DTYPE[plan.dtype]
 
 
 def rope_attn_cache_append(plan, cache, table, indptr, kv_len, spec, freqs, k, v, q=None,
@@ -604,18 +613,16 @@ def rope_attn_cache_append(plan, cache, table, indptr, kv_len, spec, freqs, k, v
     counts the appended tokens already.  Device-side faults (a bad page, length or offset, a
     value beyond the cache's range) stay in ws for rope_attn_device_status."""
     fn = "rope_attn_cache_append"
-    dev, ws, head = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)
-    dt = _CACHE_DTYPE[plan.dtype]
-    kv = torch.Size((plan.T, plan.Hkv, plan.d))
-    _vector(fn, "freqs", freqs, dev, torch.float64, (spec.rot_dim // 2,))
+    dev, head, tail, dt = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)
+    kv = (plan.T, plan.Hkv, plan.d)
+    f = _vector(fn, "freqs", freqs, dev, torch.float64, (spec.rot_dim // 2,))
     rows = [_head_rows(fn, "k", k, dev, dt, kv), _head_rows(fn, "v", v, dev, dt, kv), None, None]
     if q is not None:
-        qs = torch.Size((plan.T, plan.Hq, plan.d))
+        qs = (plan.T, plan.Hq, plan.d)
         rows[2] = _head_rows(fn, "q", q, dev, dt, qs)
         q_out = torch.empty_like(q) if q_out is None else q_out
         rows[3] = _head_rows(fn, "q_out", q_out, dev, dt, qs)
-    _call(fn, dev, *head, ctypes.byref(spec), _ptr(freqs), *[_opt(r) for r in rows], _ptr(ws),
-          ws.numel())
+    _call(fn, dev, *head, ctypes.byref(spec), f, *[_opt(r) for r in rows], *tail)
     return q_out if q is not None else None
 
 
@@ -623,13 +630,12 @@ def rope_attn_cache_read(plan, cache, table, indptr, kv_len, k=None, v=None, ws=
     """(k, v) [T, Hkv, d]: the cached rows of the batch's tokens as the values they stand for
     (for a whole cache, give indptr the running sum of kv_len)."""
     fn = "rope_attn_cache_read"
-    dev, ws, head = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)
-    dt = _CACHE_DTYPE[plan.dtype]
-    kv = torch.Size((plan.T, plan.Hkv, plan.d))
-    k = torch.empty(kv, dtype=dt, device=dev) if k is None else k
-    v = torch.empty(kv, dtype=dt, device=dev) if v is None else v
+    dev, head, tail, dt = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)
+    kv = (plan.T, plan.Hkv, plan.d)
+    k = torch.empty(kv, dtype=dt, device=cache.device) if k is None else k
+    v = torch.empty(kv, dtype=dt, device=cache.device) if v is None else v
     rows = [_head_rows(fn, "k", k, dev, dt, kv), _head_rows(fn, "v", v, dev, dt, kv)]
-    _call(fn, dev, *head, *[_opt(r) for r in rows], _ptr(ws), ws.numel())
+    _call(fn, dev, *head, ctypes.byref(rows[0]), ctypes.byref(rows[1]), *tail)
     return k, v
 
 
@@ -637,15 +643,14 @@ def rope_attn_cache_attn(plan, cache, table, indptr, kv_len, q, o=None, lse=None
     """(o [T, Hq, d], lse fp32 [T, Hq]): attention of the rotated queries q [T, Hq, d] over the
     cache.  Rows that belong to no sequence are left as they were."""
     fn = "rope_attn_cache_attn"
-    dev, ws, head = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)
-    dt = _CACHE_DTYPE[plan.dtype]
-    qs = torch.Size((plan.T, plan.Hq, plan.d))
+    dev, head, tail, dt = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)
+    T, Hq = plan.T, plan.Hq
+    qs = (T, Hq, plan.d)
     rows = _head_rows(fn, "q", q, dev, dt, qs)
-    o = torch.empty(qs, dtype=dt, device=dev) if o is None else o
-    lse = torch.empty((plan.T, plan.Hq), dtype=torch.float32, device=dev) if lse is None else lse
-    _vector(fn, "o", o, dev, dt, qs)
-    _vector(fn, "lse", lse, dev, torch.float32, (plan.T, plan.Hq))
-    _call(fn, dev, *head, ctypes.byref(rows), _ptr(o), _ptr(lse), _ptr(ws), ws.numel())
+    o = torch.empty(qs, dtype=dt, device=q.device) if o is None else o
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
+    _call(fn, dev, *head, ctypes.byref(rows), _vector(fn, "o", o, dev, dt, qs),
+          _vector(fn, "lse", lse, dev, torch.float32, (T, Hq)), *tail)
     return o, lse
 
 

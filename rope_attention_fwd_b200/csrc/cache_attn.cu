@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const AttnA
       }
     }
     for (int step = s.s0; step < s.s1; ++step) {
-      const int k0 = s.w.first + step * kStep + warp * 32;
+      const int k0 = s.key0 + step * kStep + warp * 32;
       if (k0 >= hi_all || k0 + 32 <= lo_all) continue;
       const int key = k0 + lane;
       const uint8_t* block = nullptr;  // of this lane's key
@@ -336,7 +336,10 @@ extern "C" {
 
 size_t rope_attn_cache_workspace_bytes(const ra_cache* p) {
   if (check_cache(p) != RA_OK) return 0;
-  return cache_ws(kRowsBlocks, kRowsTile, (int)p->d).total;
+  const size_t rows = cache_ws(kRowsBlocks, kRowsTile, (int)p->d).total;
+  const int64_t most = cache_dims(*p).max_q * (p->Hq / p->Hkv);
+  if (p->dtype != RA_BF16 || most <= kChunkMinRows) return rows;
+  return std::max(rows, cache_ws(kChunkBlocks, kChunkTile, (int)p->d).total);
 }
 
 ra_status rope_attn_cache_attn(const ra_cache* p, const void* cache, const int32_t* table,
@@ -364,25 +367,48 @@ ra_status rope_attn_cache_attn(const ra_cache* p, const void* cache, const int32
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t most_rows = (int64_t)a.c.max_q * (p->Hq / p->Hkv);  // of one sequence and head
 
-  const CacheWs w = cache_ws(kRowsBlocks, kRowsTile, a.c.d);
-  a.desc = reinterpret_cast<PartDesc*>(base + w.desc);
-  a.ml = reinterpret_cast<float*>(base + w.ml);
-  a.acc = reinterpret_cast<float*>(base + w.acc);
-  a.min_rows = 0, a.max_rows = int64_t(1) << 62;
-  a.min_steps = 2;
+  // One kernel and the combine of what it split; the workspace after the error word is its own
+  // until the combine has read it.
+  auto partials = [&](int blocks, int tile) {
+    const CacheWs w = cache_ws(blocks, tile, a.c.d);
+    a.desc = reinterpret_cast<PartDesc*>(base + w.desc);
+    a.ml = reinterpret_cast<float*>(base + w.ml);
+    a.acc = reinterpret_cast<float*>(base + w.acc);
+  };
+  auto combine = [&](int blocks, int64_t rows) {
+    const TimingScope timed(K_CACHE_COMBINE, s);
+    return launch_cache_combine(a, blocks, p->dtype, (int)std::min<int64_t>(rows, a.tile), s);
+  };
   cudaError_t e;
   int blocks = kRowsBlocks;
-  if (p->dtype == RA_BF16) {
-    const TimingScope timed(K_CACHE_ATTN, s);
-    e = launch_cache_rows(a, most_rows, &blocks, s);
-  } else {
-    const TimingScope timed(K_CACHE_ATTN_F32, s);
-    const int rows = (int)std::min<int64_t>(most_rows, 8);
-    e = p->d == 64 ? launch_f32<64>(a, rows, s) : launch_f32<128>(a, rows, s);
+  a.min_rows = 0, a.max_rows = int64_t(1) << 62;
+  a.min_steps = 2;
+  partials(kRowsBlocks, kRowsTile);
+  if (p->dtype == RA_F32) {
+    {
+      const TimingScope timed(K_CACHE_ATTN_F32, s);
+      const int rows = (int)std::min<int64_t>(most_rows, 8);
+      e = p->d == 64 ? launch_f32<64>(a, rows, s) : launch_f32<128>(a, rows, s);
+    }
+    if (e == cudaSuccess) e = combine(blocks, most_rows);
+    return e == cudaSuccess ? RA_OK : RA_ERR_CUDA;
   }
-  if (e != cudaSuccess) return RA_ERR_CUDA;
-  const TimingScope timed(K_CACHE_COMBINE, s);
-  e = launch_cache_combine(a, blocks, p->dtype, (int)std::min<int64_t>(most_rows, a.tile), s);
+  a.max_rows = kChunkMinRows;
+  {
+    const TimingScope timed(K_CACHE_ATTN, s);
+    e = launch_cache_rows(a, std::min<int64_t>(most_rows, kChunkMinRows), &blocks, s);
+  }
+  if (e == cudaSuccess) e = combine(blocks, most_rows);
+  if (e == cudaSuccess && most_rows > kChunkMinRows) {
+    a.min_rows = kChunkMinRows, a.max_rows = int64_t(1) << 62;
+    a.min_steps = 1;
+    partials(kChunkBlocks, kChunkTile);
+    {
+      const TimingScope timed(K_CACHE_ATTN_CHUNK, s);
+      e = launch_cache_chunk(a, s);
+    }
+    if (e == cudaSuccess) e = combine(kChunkBlocks, most_rows);
+  }
   return e == cudaSuccess ? RA_OK : RA_ERR_CUDA;
 }
 

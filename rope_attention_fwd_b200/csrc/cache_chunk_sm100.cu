@@ -1,0 +1,569 @@
+// cache_chunk_sm100.cu -- bf16 attention of prompt chunks over the paged 4-bit cache on the
+// tcgen05 tensor cores.
+//
+// Sequences with more than kChunkMinRows rows (tokens times the query heads of a kv head) come
+// here: two 128-row tiles of one item per CTA, keys in steps of 128, persistent CTAs that each
+// walk an equal run of steps (serving.h).  Bound by the tensor cores and the exponentials, like
+// the dense forward; what is new is that K and V arrive as codes.  A step's 128 keys x 2 x d
+// codes are unpacked once into shared memory for 256 query rows, by four warps of their own
+// (about 2 instructions per value beside the softmax's 3 per score), so the cache is read at
+// 4.5 bits a value and no dense copy of it exists anywhere.
+//
+// CTA = 16 warps, 1 CTA per SM (registers redistributed with setmaxnreg):
+//   warps 0-3 / 4-7   softmax of tile a / b: thread = row = TMEM lane, the row's 128 scores in
+//                     registers; they also load and convert the queries and write the output
+//   warps 8-11        unpack: thread = key; codes prefetched into registers one tile ahead,
+//                     lo + step code as fp16 into the 128-byte-swizzled operand tiles
+//   warp 12           TMEM allocator + tcgen05.mma issuer (converged warp, one elected lane)
+//   warps 13-15       idle (they complete the warpgroup that setmaxnreg acts on)
+// TMEM (512 columns): S_x at 128 x, P_x (fp16, two per column) over its first 64, O_x at
+// 256 + 128 x.  Issue order as in the dense forward: PV_x(j), then S_x(j + 1), tile by tile.
+//
+// The order of the channels inside each 16-byte unit of 8 is (0, 4, 1, 5, 2, 6, 3, 7): the
+// order in which a 32-bit word of codes unpacks two at a time.  Q, K and V all use it, so the
+// scores do not notice and the output's columns are put back when it is written.
+//
+// Numerics: q, k and v enter as fp16 (k, v rounded once from lo + step code; q converted from
+// bf16, clamped and reported as RA_ERR_RANGE beyond 65504), P as fp16, sums in fp32; lazy
+// rescale as in the dense forward (P <= 2^8).  Every wait is bounded.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math_constants.h>
+
+#include "cache_attn.h"
+#include "cache_sched.cuh"
+#include "common.h"
+#include "launch.h"
+#include "sm100.cuh"
+
+namespace ra {
+namespace {
+
+template <int D>
+struct ChunkCfg {
+  static constexpr int NSK = 2, NSV = 2;                  // K and V ring stages
+  static constexpr int CH = D / 64;                       // 64-channel chunks per row
+  static constexpr uint32_t CHUNK = 128u * 128u;          // [128 rows][128 B]
+  static constexpr uint32_t TILE = CHUNK * CH;            // [128][D] fp16
+  static constexpr uint32_t OFF_Q = 0;                    // tiles a, b
+  static constexpr uint32_t OFF_K = 2 * TILE;
+  static constexpr uint32_t OFF_V = OFF_K + NSK * TILE;
+  static constexpr uint32_t OFF_BAR = OFF_V + NSV * TILE;
+  static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;  // + alignment slack
+  static constexpr uint32_t COL_S = 0, COL_O = 256;
+};
+
+enum ChunkBar {
+  B_Q_FULL = 0,   // both tiles' queries are in shared memory; 8 warp arrivals
+  B_K_FULL = 1,   // +stage: unpacked; 4 warp arrivals
+  B_K_EMPTY = 3,  // +stage: the S products that read it are done
+  B_V_FULL = 5,
+  B_V_EMPTY = 7,
+  B_S_FULL = 9,   // +tile
+  B_P_FULL = 11,  // +tile: P written and O rescaled; 4 warp arrivals
+  B_PV_DONE = 13, // +tile
+  B_O_DONE = 15,  // every product of the segment is done
+  B_DRAIN = 16,
+  B_COUNT = 17
+};
+
+constexpr int kThreads = 512;
+constexpr int kUnpackWarp = 8, kMmaWarp = 12;
+constexpr float kTau = 8.0f;
+
+// registers per thread after the redistribution: 256 x 184 + 128 x 88 + 128 x 56 = 65,536
+#define RA_SETMAXNREG_INC(n) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n))
+#define RA_SETMAXNREG_DEC(n) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n))
+
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
+  return y;
+}
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+
+// The steps [j0, j1) of a segment in which row tile x (rows x 128 .. of the item's) sees a key.
+struct StepRange {
+  int j0, j1;
+};
+__device__ __forceinline__ StepRange tile_steps(const CacheDims& c, const Segment& s, int x,
+                                                int rows) {
+  const long long row0 = (long long)s.tile * kChunkTile;
+  if (rows <= 128 * x) return {s.s0, s.s0};
+  const KeyRange f = row_keys(c, s.w, row0 + 128 * x, s.w.G);
+  const KeyRange l = row_keys(c, s.w, row0 + min(rows, 128 * x + 128) - 1, s.w.G);
+  StepRange r{s.s0, s.s1};
+  if (l.hi <= s.key0) return {s.s0, s.s0};
+  r.j1 = min(r.j1, (l.hi - s.key0 + kStep - 1) / kStep);
+  if (f.lo > s.key0) r.j0 = max(r.j0, (f.lo - s.key0) / kStep);
+  if (r.j1 < r.j0) r.j1 = r.j0;
+  return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const AttnArgs a) {
+  using C = ChunkCfg<D>;
+  constexpr int KID = K_CACHE_ATTN_CHUNK;
+  constexpr int NG = D / kGroup;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ long long scratch[kThreads / 32 + 4];
+  const uint32_t raw_s = smem_u32(smem_raw);
+  const uint32_t base_s = (raw_s + 1023u) & ~1023u;
+  uint8_t* base = smem_raw + (base_s - raw_s);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(base + C::OFF_BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::OFF_BAR + 8 * B_COUNT);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + C::OFF_BAR + 8 * B_COUNT + 4);
+  const CacheDims& c = a.c;
+  const int G = c.Hq / c.Hkv;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < B_COUNT; ++i) {
+      const int n = i == B_Q_FULL ? 8
+                    : (i == B_K_FULL || i == B_K_FULL + 1 || i == B_V_FULL ||
+                       i == B_V_FULL + 1 || i == B_P_FULL || i == B_P_FULL + 1)
+                        ? 4
+                        : 1;
+      mbar_init(&bar[i], n);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  const Run run = find_run(a, scratch, KID);
+  // a block without work (an idle one of a small launch) takes no TMEM and waits for nothing
+  if (run.begin >= run.end) {
+    if (threadIdx.x == 0) a.desc[blockIdx.x] = PartDesc{0, 0, 0, 0};
+    return;
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  Walk<WorkOf> walk(WorkOf{a}, run, c.B);
+  Segment s;
+  auto rows_of = [&](const Segment& g) {
+    return (int)min((long long)kChunkTile,
+                    (long long)g.w.qn * G - (long long)g.tile * kChunkTile);
+  };
+
+  if (warp >= kMmaWarp) {
+    RA_SETMAXNREG_DEC(56);
+    if (warp == kMmaWarp) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t idS = idesc_f16_f32(128, 128, 0, 0);
+      constexpr uint32_t idO = idesc_f16_f32(128, D, 0, 1);
+      const SDesc dkm = sdesc_split(base_s, 16, 1024);        // K-major tiles
+      const SDesc dmn = sdesc_split(base_s, C::CHUNK, 1024);  // V tiles read MN-major
+      uint32_t nk = 0, nv = 0, seg = 0;  // K tiles, V tiles and segments so far
+      uint32_t np[2] = {0u, 0u};         // P tiles of each row tile so far
+      bool ok = true;
+      while (ok && walk.next(s)) {
+        const int rows = rows_of(s);
+        const StepRange ra_ = tile_steps(c, s, 0, rows), rb = tile_steps(c, s, 1, rows);
+        int j0 = ra_.j0, j1 = ra_.j1;
+        if (rb.j0 < rb.j1) {
+          j0 = j0 < j1 ? min(j0, rb.j0) : rb.j0;
+          j1 = max(j1, rb.j1);
+        }
+        if (j0 >= j1) continue;
+        auto active = [&](int x, int j) {
+          return x == 0 ? j >= ra_.j0 && j < ra_.j1 : j >= rb.j0 && j < rb.j1;
+        };
+        if (!(ok = mbar_wait_warp(&bar[B_Q_FULL], seg & 1, abort_flag, a.err, KID, 1, a.wait_ns)))
+          break;
+        ++seg;
+        tc_fence_after();
+        auto issue_s = [&](int x, uint32_t k) {
+          const SDesc ks = sdesc_advance(dkm, C::OFF_K + (k % C::NSK) * C::TILE);
+          const uint32_t q_off = C::OFF_Q + x * C::TILE;
+          if constexpr (D == 128)
+            mma8_kmajor<false, C::CHUNK, C::CHUNK>(tmem + C::COL_S + x * 128,
+                                                   sdesc_at(dkm, q_off), sdesc_at(ks, 0), idS, 0);
+          else
+            mma4_kmajor<false>(tmem + C::COL_S + x * 128, sdesc_at(dkm, q_off), sdesc_at(ks, 0),
+                               idS, 0);
+          mma_commit_warp(&bar[B_S_FULL + x]);
+        };
+        auto wait_k = [&](uint32_t k) -> bool {
+          if (!mbar_wait_warp(&bar[B_K_FULL + k % C::NSK], (k / C::NSK) & 1, abort_flag, a.err,
+                              KID, 2, a.wait_ns))
+            return false;
+          tc_fence_after();
+          return true;
+        };
+        if (!(ok = wait_k(nk))) break;
+        for (int x = 0; x < 2; ++x)
+          if (active(x, j0)) issue_s(x, nk);
+        mma_commit_warp(&bar[B_K_EMPTY + nk % C::NSK]);
+        ++nk;
+        for (int j = j0; ok && j < j1; ++j) {
+          const bool next = j + 1 < j1;
+          if (next && !(ok = wait_k(nk))) break;
+          if (!(ok = mbar_wait_warp(&bar[B_V_FULL + nv % C::NSV], (nv / C::NSV) & 1, abort_flag,
+                                    a.err, KID, 3, a.wait_ns)))
+            break;
+          for (int x = 0; x < 2; ++x) {
+            if (active(x, j)) {
+              if (!(ok = mbar_wait_warp(&bar[B_P_FULL + x], np[x] & 1, abort_flag, a.err, KID, 4,
+                                        a.wait_ns)))
+                break;
+              ++np[x];
+              tc_fence_after();
+              const SDesc vs = sdesc_advance(dmn, C::OFF_V + (nv % C::NSV) * C::TILE);
+              mma8_ts_mn(tmem + C::COL_O + x * 128, tmem + C::COL_S + x * 128, sdesc_at(vs, 0),
+                         idO, j > (x == 0 ? ra_.j0 : rb.j0));
+              mma_commit_warp(&bar[B_PV_DONE + x]);
+            }
+            if (next && active(x, j + 1)) issue_s(x, nk);
+          }
+          if (!ok) break;
+          mma_commit_warp(&bar[B_V_EMPTY + nv % C::NSV]);
+          ++nv;
+          if (next) {
+            mma_commit_warp(&bar[B_K_EMPTY + nk % C::NSK]);
+            ++nk;
+          }
+        }
+        if (ok) mma_commit_warp(&bar[B_O_DONE]);
+      }
+      // every product issued above has finished once this commit arrives
+      mma_commit_warp(&bar[B_DRAIN]);
+      int dummy = 0;
+      mbar_wait_warp(&bar[B_DRAIN], 0, &dummy, a.err, KID, 5, a.wait_ns);
+    }
+  } else if (warp >= kUnpackWarp) {
+    // -------------------------------------------------------------- unpack: thread = key
+    RA_SETMAXNREG_DEC(88);
+    const int key_t = threadIdx.x - kUnpackWarp * 32;
+    const uint32_t row_off = key_t * 128u;
+    uint32_t nk = 0, nv = 0;
+    bool ok = true;
+    uint4 codes[2][D / 32];  // [K, V] of the next tile
+    uint32_t pairs[2][NG];
+    while (ok && walk.next(s)) {
+      const int rows = rows_of(s);
+      const StepRange r0 = tile_steps(c, s, 0, rows), r1 = tile_steps(c, s, 1, rows);
+      int j0 = r0.j0, j1 = r0.j1;
+      if (r1.j0 < r1.j1) {
+        j0 = j0 < j1 ? min(j0, r1.j0) : r1.j0;
+        j1 = max(j1, r1.j1);
+      }
+      if (j0 >= j1) continue;
+      // page of this thread's key in step j (-1: behind the last token, or a bad page)
+      auto page_at = [&](int j) -> int {
+        const int key = s.key0 + j * kStep + key_t;
+        if (j >= j1 || key >= s.w.L) return -1;
+        return page_of(c, a.table, s.b, key / kBlock, a.err, KID);
+      };
+      auto load = [&](int z, int j, int page) {  // z: 0 K, 1 V
+        const int key = s.key0 + j * kStep + key_t;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) pairs[z][g] = 0u;  // masked keys: value 0
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) codes[z][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (page < 0) return;
+        const uint8_t* block = a.cache + block_at(c, page, s.h, key / kBlock % c.page_blocks) +
+                               z * value_offset(D);
+        const uint4* src = reinterpret_cast<const uint4*>(block + key % kBlock * (D / 2));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) codes[z][i] = src[i];
+        const uint32_t* p =
+            reinterpret_cast<const uint32_t*>(block + code_bytes(D)) + key % kBlock * NG;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) pairs[z][g] = p[g];
+      };
+      auto unpack = [&](int z, uint32_t tile) {  // into the tile at shared address `tile`
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const __half2 step = as_half2(__byte_perm(pairs[z][g], 0, 0x1010)),
+                        lo = as_half2(__byte_perm(pairs[z][g], 0, 0x3232));
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const uint4 w4 = codes[z][g * 2 + u / 4];
+            const uint32_t w = u % 4 == 0 ? w4.x : u % 4 == 1 ? w4.y : u % 4 == 2 ? w4.z : w4.w;
+            uint32_t v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __half2 cd = as_half2(and_or(w >> (4 * i), 0x000f000fu, 0x64006400u));
+              v[i] = as_u32(__hfma2(__hsub2(cd, as_half2(0x64006400u)), step, lo));
+            }
+            st_shared_v4(tile + g * C::CHUNK + row_off + ((u ^ (key_t & 7)) << 4), v[0], v[1],
+                         v[2], v[3]);
+          }
+        }
+      };
+      int page = page_at(j0), page_next = page_at(j0 + 1);
+      load(0, j0, page);
+      load(1, j0, page);
+      for (int j = j0; j < j1; ++j) {
+        const uint32_t sk = nk % C::NSK, sv = nv % C::NSV;
+        if (!(ok = mbar_wait_warp(&bar[B_K_EMPTY + sk], ((nk / C::NSK) & 1) ^ 1, abort_flag, a.err,
+                                  KID, 6, a.wait_ns)))
+          break;
+        unpack(0, base_s + C::OFF_K + sk * C::TILE);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[B_K_FULL + sk]);
+        ++nk;
+        if (j + 1 < j1) load(0, j + 1, page_next);
+        if (!(ok = mbar_wait_warp(&bar[B_V_EMPTY + sv], ((nv / C::NSV) & 1) ^ 1, abort_flag, a.err,
+                                  KID, 7, a.wait_ns)))
+          break;
+        unpack(1, base_s + C::OFF_V + sv * C::TILE);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[B_V_FULL + sv]);
+        ++nv;
+        if (j + 1 < j1) load(1, j + 1, page_next);
+        page = page_next;
+        page_next = page_at(j + 2);
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- softmax: thread = row
+    RA_SETMAXNREG_INC(184);
+    const int x = warp / 4;            // row tile a (0) or b (1)
+    const int t = threadIdx.x % 128;   // row of the tile == TMEM lane
+    const uint32_t lane_base = tmem + ((uint32_t)((warp % 4) * 32) << 16);
+    const uint32_t s_base = lane_base + C::COL_S + x * 128;
+    const uint32_t o_base = lane_base + C::COL_O + x * 128;
+    const float scale_log2 = c.scale * 1.4426950408889634f;
+    uint32_t ns = 0, seg = 0;          // S tiles of this row tile, segments with products so far
+    int followers = 0, fb = 0, fh = 0, ft = 0;
+    bool ok = true;
+    while (ok && walk.next(s)) {
+      const int rows = rows_of(s);
+      const StepRange r0 = tile_steps(c, s, 0, rows), r1 = tile_steps(c, s, 1, rows);
+      const bool any = r0.j0 < r0.j1 || r1.j0 < r1.j1;
+      const StepRange mine = x == 0 ? r0 : r1;
+      const int r = 128 * x + t;       // row of the item's tile
+      const long long row = (long long)s.tile * kChunkTile + r;
+      const bool live = r < rows;
+      const KeyRange kr = live ? row_keys(c, s.w, row, G) : KeyRange{0, 0};
+      const long long token = s.w.q0 + (live ? row / G : 0);
+      const long long head = (long long)s.h * G + (live ? row % G : 0);
+      // keys that every live row of the tile sees (both ends rise with the row): a step inside
+      // needs no mask
+      const int last_r = max(0, min(rows, 128 * x + 128) - 1);
+      const KeyRange tf = row_keys(c, s.w, (long long)s.tile * kChunkTile + 128 * x, G);
+      const KeyRange tl = row_keys(c, s.w, (long long)s.tile * kChunkTile + last_r, G);
+      if (any) {
+        // the row's query as fp16, in the unpacked channel order, into the swizzled tile
+        const uint32_t tile = base_s + C::OFF_Q + x * C::TILE + t * 128u;
+        const __nv_bfloat16* src =
+            static_cast<const __nv_bfloat16*>(a.q) + token * a.q_n + head * a.q_h;
+        bool beyond = false;
+#pragma unroll 4
+        for (int u = 0; u < D / 8; ++u) {
+          uint32_t w[4] = {0u, 0u, 0u, 0u};
+          if (live) {
+            if (a.q_vec) {
+              const uint4 v = reinterpret_cast<const uint4*>(src)[u];
+              w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+            } else {
+              const uint16_t* h = reinterpret_cast<const uint16_t*>(src) + 8 * u;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) w[e] = h[2 * e] | ((uint32_t)h[2 * e + 1] << 16);
+            }
+          }
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[2 * e] = __uint_as_float(w[e] << 16);
+            f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) beyond = beyond || !(fabsf(f[e]) <= 65504.f);
+          st_shared_v4(tile + (u / 8) * C::CHUNK + (((u % 8) ^ (t & 7)) << 4),
+                       pack_f16x2_sat(f[0], f[4]), pack_f16x2_sat(f[1], f[5]),
+                       pack_f16x2_sat(f[2], f[6]), pack_f16x2_sat(f[3], f[7]));
+        }
+        if (beyond) atomicCAS(a.err, 0u, (uint32_t)RA_ERR_RANGE);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[B_Q_FULL]);
+      }
+      float m = -CUDART_INF_F, l = 0.f;
+      // blocks of 16 keys of a step that hold readable keys (bad pages count as masked)
+      auto readable = [&](int j) -> uint32_t {
+        const int key = s.key0 + j * kStep + lane * kBlock;
+        const bool good =
+            lane < kStep / kBlock && key < s.w.L &&
+            page_ok(c, a.table[(long long)s.b * c.max_pages + key / kBlock / c.page_blocks]);
+        return __ballot_sync(0xffffffffu, good || lane >= kStep / kBlock || key >= s.w.L);
+      };
+      for (int j = mine.j0; j < mine.j1; ++j) {
+        const uint32_t blocks = readable(j);
+        if (!mbar_wait_warp(&bar[B_S_FULL + x], ns & 1, abort_flag, a.err, KID, 8, a.wait_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(s_base + 32 * q, sr[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_wait_ld(sr[q]);
+        const int k0 = s.key0 + j * kStep;
+        if (k0 < tl.lo || k0 + kStep > tf.hi || blocks != 0xffffffffu) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int key = k0 + 32 * q + i;
+              if (key < kr.lo || key >= kr.hi || !(blocks >> (2 * q + i / 16) & 1))
+                sr[q][i] = __float_as_uint(-CUDART_INF_F);
+            }
+        }
+        auto sv = [&](int i) { return __uint_as_float(sr[i / 32][i % 32]); };
+        float mp[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float v = fmax3(sv(e), sv(e + 8), sv(e + 16));
+#pragma unroll
+          for (int i = 24; i < 120; i += 16) v = fmax3(v, sv(e + i), sv(e + i + 8));
+          mp[e] = fmaxf(v, sv(e + 120));
+        }
+        const float mt = fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]),
+                               fmaxf(mp[6], mp[7])) * scale_log2;
+        // scale may be negative or zero in principle: the maximum is taken of the products
+        const bool rescale = __any_sync(0xffffffffu, mt > m + kTau);
+        if (rescale) {
+          const float mn = fmaxf(m, mt);
+          const float corr = mn == -CUDART_INF_F ? 1.f : fast_exp2(m - mn);
+          m = mn;
+          l *= corr;
+          if (j > mine.j0) {
+            // O must hold every product issued so far
+            if (!mbar_wait_warp(&bar[B_PV_DONE + x], (ns - 1) & 1, abort_flag, a.err, KID, 9,
+                                a.wait_ns)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t v[32];
+              tmem_ld32(o_base + 32 * q, v);
+              tmem_wait_ld(v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * corr);
+              tmem_st32(o_base + 32 * q, v);
+            }
+          }
+        }
+        const float mu = m == -CUDART_INF_F ? 0.f : m;
+        float2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 e = ffma2(make_float2(sv(32 * q + 2 * i), sv(32 * q + 2 * i + 1)),
+                                   make_float2(scale_log2, scale_log2), make_float2(-mu, -mu));
+            const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+            sum[i % 4] = fadd2(sum[i % 4], p);
+            w[i] = as_u32(__floats2half2_rn(p.x, p.y));
+          }
+          tmem_st16(s_base + 16 * q, w);
+        }
+        const float2 tot = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+        l += tot.x + tot.y;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[B_P_FULL + x]);
+        ++ns;
+      }
+      if (!ok) break;
+      if (any) {
+        if (!mbar_wait_warp(&bar[B_O_DONE], seg & 1, abort_flag, a.err, KID, 10, a.wait_ns)) {
+          ok = false;
+          break;
+        }
+        ++seg;
+        tc_fence_after();
+      }
+      const bool whole = s.first && s.last;
+      const long long slot = 2ll * blockIdx.x + (s.first ? 1 : 0);
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const bool seen = mine.j0 < mine.j1;  // O holds something
+      const long long at = whole ? token * c.Hq + head : slot * kChunkTile + r;
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t v[32];
+        if (seen) {
+          tmem_ld32(o_base + 32 * q, v);
+          tmem_wait_ld(v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
+        }
+        if (!live) continue;
+        const float* f = reinterpret_cast<const float*>(v);
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at * D + 32 * q);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)   // columns hold channels 0, 4, 1, 5, 2, 6, 3, 7 of eight
+            dst[u] = make_uint4(pack_bf16x2(f[8 * u] * inv, f[8 * u + 2] * inv),
+                                pack_bf16x2(f[8 * u + 4] * inv, f[8 * u + 6] * inv),
+                                pack_bf16x2(f[8 * u + 1] * inv, f[8 * u + 3] * inv),
+                                pack_bf16x2(f[8 * u + 5] * inv, f[8 * u + 7] * inv));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(a.acc + at * D + 32 * q);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            dst[2 * u] = make_float4(f[8 * u], f[8 * u + 2], f[8 * u + 4], f[8 * u + 6]);
+            dst[2 * u + 1] = make_float4(f[8 * u + 1], f[8 * u + 3], f[8 * u + 5], f[8 * u + 7]);
+          }
+        }
+      }
+      if (live) {
+        if (whole) {
+          a.lse[at] = (m + log2f(l)) * 0.6931471805599453f;
+        } else {
+          a.ml[at * 2] = m;
+          a.ml[at * 2 + 1] = l;
+        }
+      }
+      if (s.followers) followers = s.followers, fb = s.b, fh = s.h, ft = s.tile;
+      // the next segment's products overwrite O and the queries only after this warp's arrival
+      // on its P and Q barriers
+      tc_fence_before();
+    }
+    if (threadIdx.x == 0) a.desc[blockIdx.x] = PartDesc{ok ? followers : 0, fb, fh, ft};
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <int D>
+cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
+  using C = ChunkCfg<D>;
+  const cudaError_t e = cudaFuncSetAttribute(
+      cache_attn_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  cache_attn_chunk_kernel<D><<<kChunkBlocks, kThreads, C::SMEM, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_chunk(AttnArgs& a, cudaStream_t s) {
+  a.tile = kChunkTile;
+  return a.c.d == 64 ? launch<64>(a, s) : launch<128>(a, s);
+}
+
+}  // namespace ra

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
       }
     const KeyRange kf = row_keys(c, s.w, row0, G), kl = row_keys(c, s.w, row0 + rows - 1, G);
     // this warp's shares of the segment's steps that hold a visible key: [i0, i1)
-    const int base = s.w.first + warp * 32;   // key of share 0
+    const int base = s.key0 + warp * 32;   // key of share 0
     int i0 = s.s0, i1 = s.s1;
     if (kl.hi <= base) i1 = i0;
     else i1 = min(i1, (kl.hi - base + kStep - 1) / kStep);

@@ -56,7 +56,7 @@ __host__ __device__ inline int sequence_fault(const CacheDims& c, int q0, int q1
 
 // ------------------------------------------------------------------ pieces of attention work
 // The rows of a sequence that share a kv head are its tokens times the G = Hq / Hkv query
-// heads (row = token * G + head of the group), cut into tiles of `tile` rows.  An item is one
+// heads (row = token * G + head of the group), cut into tiles of R rows.  An item is one
 // (sequence, kv head, row tile); its keys are walked in steps of kStep tokens.  All items'
 // steps are numbered through (sequences, then heads, then row tiles, then steps) and dealt out
 // in equal runs of `per` steps to the blocks of a launch of fixed size, whatever the lengths:
@@ -65,33 +65,75 @@ __host__ __device__ inline int sequence_fault(const CacheDims& c, int q0, int q1
 // kernel from fp32 partial sums.
 constexpr int kStep = 128;
 
+// sum of floor(a t / m) over t = 0..k, a in {1, 2}
+__host__ __device__ inline long long floor_sum(long long k, int a, long long m) {
+  if (a == 2 && m % 2 == 0) a = 1, m /= 2;
+  const long long q = k / m, r = k - q * m;
+  if (a == 1) return m * (q * (q - 1) / 2) + q * (r + 1);
+  if (m == 1) return k * (k + 1);
+  const long long half = (m + 1) / 2;  // the first t of a period with 2 t >= m
+  return q * (q - 1) * m + q * ((m - 1) / 2) + 2 * q * (r + 1) + (r >= half ? r - half + 1 : 0);
+}
+
 struct SeqWork {
-  int q0, qn, L;     // first row in the batch, tokens, cached tokens
-  int first;         // first key of the first step (a multiple of kBlock)
-  int steps;         // steps of an item (0: no item)
-  int tiles;         // row tiles
-  long long total;   // steps of the sequence over all heads and tiles
+  int q0, qn, L;      // first row in the batch, tokens, cached tokens
+  int tiles;          // row tiles
+  int steps;          // steps of every item, or (rising) before the tile's own share
+  int rising;         // causal, several tiles: tile t takes steps + floor(a (t + 1) / m) + 1
+  int a, m;
+  int window;         // > 0: every tile starts at its own first visible key
+  int R, G;
+  long long per_head; // steps of all tiles of one head
+  long long total;    // and of all heads
+
+  __host__ __device__ int tile_steps(int t) const {
+    return rising ? steps + (int)((long long)a * (t + 1) / m) + 1 : steps;
+  }
+  // steps of the tiles before t
+  __host__ __device__ long long steps_before(int t) const {
+    return rising ? (long long)t * (steps + 1) + floor_sum(t, a, m) : (long long)t * steps;
+  }
+  // first key of the tile's first step, a multiple of kBlock
+  __host__ __device__ int tile_first(int t) const {
+    if (window == 0) return 0;
+    const long long row = (long long)t * R;
+    const long long b = (long long)L - qn + row / G - window + 1;
+    return b > 0 ? (int)(b < L ? b : L) / kBlock * kBlock : 0;
+  }
 };
 
-// The steps of sequence (q0, q1, L) for a kernel that takes sequences of min_rows < rows <=
-// max_rows; none if the sequence is faulty, empty or another kernel's.
-__host__ __device__ inline SeqWork seq_work(const CacheDims& c, int q0, int q1, int L, int tile,
+// The steps of sequence (q0, q1, L) for a kernel with tiles of R rows that takes sequences of
+// min_rows < rows <= max_rows; none if the sequence is faulty, empty or another kernel's.
+// R is 1, 2, 4, .. 128 or 256.
+__host__ __device__ inline SeqWork seq_work(const CacheDims& c, int q0, int q1, int L, int R,
                                             long long min_rows, long long max_rows) {
-  SeqWork w{q0, 0, L, 0, 0, 0, 0};
+  SeqWork w{};
+  w.q0 = q0, w.L = L, w.R = R, w.G = c.Hq / c.Hkv;
   if (sequence_fault(c, q0, q1, L) || q1 == q0) return w;
-  const long long rows = (long long)(q1 - q0) * (c.Hq / c.Hkv);
+  const long long rows = (long long)(q1 - q0) * w.G;
   if (rows <= min_rows || rows > max_rows) return w;
   w.qn = q1 - q0;
-  int begin = 0;
-  if (c.causal && c.window > 0) {  // the first token's window
-    const long long b = (long long)L - w.qn - c.window + 1;
-    begin = b > 0 ? (int)(b < L ? b : L) : 0;
+  w.tiles = (int)((rows + R - 1) / R);
+  const int all = (L + kStep - 1) / kStep;
+  if (c.causal && c.window > 0) {
+    // 15 keys of alignment, the first row's window, the tile's further tokens
+    const long long span = 15ll + c.window + (R - 1) / w.G + 1;
+    const long long n = (span + kStep - 1) / kStep;
+    w.window = c.window;
+    w.steps = n < all ? (int)n : all;
+  } else if (c.causal && w.tiles > 1) {
+    // tile t's last row sees L - qn + floor((R (t + 1) - 1) / G) + 1 keys: at most
+    // ceil((L - qn) / kStep) + floor(R (t + 1) / (kStep G)) + 1 steps
+    w.rising = 1;
+    w.a = R > kStep ? R / kStep : 1;
+    w.m = R > kStep ? w.G : kStep / R * w.G;
+    w.steps = L > w.qn ? (L - w.qn + kStep - 1) / kStep : 0;
+  } else {
+    w.steps = all;
   }
-  w.first = begin / kBlock * kBlock;
-  w.steps = (L - w.first + kStep - 1) / kStep;
-  if (w.steps < 1) w.steps = 1;  // no key: one empty step writes the rows
-  w.tiles = (int)((rows + tile - 1) / tile);
-  w.total = (long long)c.Hkv * w.tiles * w.steps;
+  if (!w.rising && w.steps < 1) w.steps = 1;  // no key: one empty step writes the rows
+  w.per_head = w.steps_before(w.tiles);
+  w.total = c.Hkv * w.per_head;
   return w;
 }
 
@@ -111,7 +153,8 @@ struct Run {
 // One item's share of a block's run.
 struct Segment {
   int b, h, tile;
-  int s0, s1;            // its steps [s0, s1) of w.steps
+  int s0, s1;            // its steps [s0, s1)
+  int key0;              // first key of the item's step 0
   bool first, last;      // holds the item's first / last step
   int followers;         // first and not last: blocks after this one that go on with it
   SeqWork w;
@@ -120,37 +163,58 @@ struct Segment {
 // Walks the segments of a run in order; next() is uniform over the block.
 template <typename F>
 struct Walk {
-  long long at, end, base, per;
-  int b, B;
+  long long at, end, per;
+  long long item;        // the total's number of the current item's first step
+  int b, h, tile, n, B;  // the current item, its steps; sequences
   SeqWork w;
-  F work;  // sequence number -> SeqWork
+  F work;                // sequence number -> SeqWork
 
   __host__ __device__ Walk(const F& f, const Run& r, int sequences)
-      : at(r.begin), end(r.end), base(r.base), per(r.per), b(r.b), B(sequences), work(f) {
-    if (at < end) w = work(b);
+      : at(r.begin), end(r.end), per(r.per), item(r.base), b(r.b), h(0), tile(0), n(0),
+        B(sequences), work(f) {
+    if (at >= end) return;
+    w = work(b);
+    const long long rel = at - r.base;
+    h = (int)(rel / w.per_head);
+    const long long x = rel - h * w.per_head;
+    int lo = 0, hi = w.tiles;  // the last tile with steps_before <= x
+    if (!w.rising) {
+      lo = (int)(x / w.steps);
+    } else {
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (w.steps_before(mid) <= x) lo = mid;
+        else hi = mid;
+      }
+    }
+    tile = lo;
+    n = w.tile_steps(tile);
+    item = r.base + h * w.per_head + w.steps_before(tile);
   }
   __host__ __device__ bool next(Segment& s) {
     if (at >= end) return false;
-    while (at >= base + w.total) {  // at < end <= total: a later sequence holds it
-      base += w.total;
-      if (++b >= B) return false;
-      w = work(b);
+    while (at >= item + n) {  // at < end <= total: a later item holds it
+      item += n;
+      if (++tile >= w.tiles) {
+        tile = 0;
+        if (++h >= w.total / (w.per_head > 0 ? w.per_head : 1)) {
+          h = 0;
+          do {
+            if (++b >= B) return false;
+            w = work(b);
+          } while (w.total == 0);
+        }
+      }
+      n = w.tile_steps(tile);
     }
-    const long long rel = at - base;
-    const long long item = rel / w.steps;
-    s.b = b;
-    s.h = (int)(item / w.tiles);
-    s.tile = (int)(item - (long long)s.h * w.tiles);
-    s.s0 = (int)(rel - item * w.steps);
+    s.b = b, s.h = h, s.tile = tile;
+    s.s0 = (int)(at - item);
     const long long left = end - at;
-    s.s1 = left < w.steps - s.s0 ? s.s0 + (int)left : w.steps;
+    s.s1 = left < n - s.s0 ? s.s0 + (int)left : n;
+    s.key0 = w.tile_first(tile);
     s.first = s.s0 == 0;
-    s.last = s.s1 == w.steps;
-    s.followers = 0;
-    if (s.first && !s.last) {
-      const long long item_end = base + (item + 1) * w.steps;
-      s.followers = (int)((item_end - 1) / per - at / per);
-    }
+    s.last = s.s1 == n;
+    s.followers = s.first && !s.last ? (int)((item + n - 1) / per - at / per) : 0;
     s.w = w;
     at += s.s1 - s.s0;
     return true;

@@ -47,10 +47,20 @@ static int check_cut(const ra::CacheDims& c, const Batch& t, int blocks, int til
     int segments = 0, split_here = 0;
     while (walk.next(s)) {
       const ra::SeqWork w = work(s.b);
+      const int n = w.tiles > s.tile ? w.tile_steps(s.tile) : 0;
       if (s.h < 0 || s.h >= c.Hkv || s.tile < 0 || s.tile >= w.tiles || s.s0 < 0 ||
-          s.s0 >= s.s1 || s.s1 > w.steps)
+          s.s0 >= s.s1 || s.s1 > n)
         return fail("segment range", blk, s.b, s.s0);
-      const long long item = base[s.b] + ((long long)s.h * w.tiles + s.tile) * w.steps;
+      const long long item = base[s.b] + s.h * w.per_head + w.steps_before(s.tile);
+      if (w.steps_before(s.tile + 1) - w.steps_before(s.tile) != n)
+        return fail("steps_before", s.b, s.tile, n);
+      // the tile's steps hold every key that one of its rows sees
+      const long long row0 = (long long)s.tile * tile, rows = (long long)w.qn * w.G;
+      const long long row1 = row0 + tile < rows ? row0 + tile - 1 : rows - 1;
+      const ra::KeyRange k0 = ra::row_keys(c, w, row0, w.G), k1 = ra::row_keys(c, w, row1, w.G);
+      if (s.key0 % ra::kBlock || s.key0 < 0 || (k0.lo < k0.hi && s.key0 > k0.lo) ||
+          k1.hi > s.key0 + (long long)n * ra::kStep)
+        return fail("keys outside the steps", s.b, s.tile, k1.hi);
       for (int k = s.s0; k < s.s1; ++k) {
         if (seen[(size_t)(item + k)]++) return fail("step twice", blk, s.b, k);
         owner[(size_t)(item + k)] = blk;
@@ -61,7 +71,7 @@ static int check_cut(const ra::CacheDims& c, const Batch& t, int blocks, int til
       if (!s.last) split_here = 1;
       if (s.first && !s.last) {
         if (s.followers < 1) return fail("no followers", blk, s.b, s.s0);
-        splits.push_back({item + w.steps, blk, s.followers});
+        splits.push_back({item + n, blk, s.followers});
       } else if (s.followers) {
         return fail("followers of a whole item", blk, s.b, s.followers);
       }
@@ -85,6 +95,7 @@ int main() {
   unsigned seed = 12345;
   auto rnd = [&](int n) { return (int)((seed = seed * 1664525u + 1013904223u) >> 8) % n; };
   for (int trial = 0; trial < 400; ++trial) {
+    c.Hkv = 1 + trial % 2, c.Hq = c.Hkv * (1 + rnd(8));
     c.B = trial % 7 == 0 ? 1 : 1 + rnd(trial % 5 == 0 ? 300 : 20);
     c.window = trial % 4 == 1 ? 1 + rnd(5000) : 0;
     c.causal = trial % 6 != 5 || c.window;
@@ -104,6 +115,15 @@ int main() {
         if (check_cut(c, t, blocks, tile, 2, 0, 64)) return 1;
       }
   }
+  for (int a : {1, 2})
+    for (int m = 1; m < 40; ++m) {
+      long long sum = 0;
+      for (int t = 0; t < 300; ++t) {
+        sum += (long long)a * t / m;
+        if (ra::floor_sum(t, a, m) != sum) return fail("floor_sum", t, a, m);
+      }
+    }
+  c.Hq = 8, c.Hkv = 2;
   // faults: nothing of a faulty sequence is ever followed
   c.B = 1, c.window = 0, c.causal = 1, c.T = 100, c.max_q = 50, c.max_pages = 4, c.pages = 7;
   struct F { int q0, q1, L, want; };
@@ -134,7 +154,6 @@ int main() {
               const bool see = !causal || (j <= pos && (!win || j > pos - win));
               n += see;
               if (see != (j >= k.lo && j < k.hi)) return fail("row_keys", L, row, j);
-              if (see && j < w.first) return fail("key before the first step", L, row, j);
             }
             if (n == 0 && k.lo < k.hi) return fail("empty row", L, row, k.lo);
           }

@@ -93,7 +93,9 @@ class Batch:
             biased in the products) =: ds, which moves p by 2 ds relative (numerator and sum);
           exp2 and the sums of p: 2^-20 relative (2 ulp of ex2.approx, rescales, sums of at
             most 2^11 terms per lane and step in fp32);
-          bf16: p and v are rounded to fp16 (2^-11 each; below 2^-14 by at most 2^-25 absolute).
+          bf16: p and v are rounded to fp16 (2^-11 each; below 2^-14 by at most 2^-25 absolute);
+          bf16, more than 64 rows per kv head: k is rounded to fp16 too (2^-11 relative, or 2^-25),
+            which moves a score by at most scale sum |q| (2^-11 |k| + 2^-25), added to ds.
         All of it relative to sum_j p_j |v_j|; lse moves by ds + 2^-20 and its own rounding."""
         U, bf = 2.0 ** -24, self.dtype == torch.bfloat16
         q = self.q.double().numpy() if q is None else q
@@ -109,6 +111,8 @@ class Batch:
             kmax = np.nanmax(abs(k)) if k.size and not np.isnan(k).all() else 0.0
             q1 = abs(q[at]).sum(-1)
             ds = ((self.d + 16) * U * scale * q1 * kmax * 18)[..., None]
+            if bf and n * (self.Hq // self.Hkv) > 64:
+                ds = ds + (scale * q1 * (2.0 ** -11 * kmax + 2.0 ** -25))[..., None]
             vmax = np.nanmax(abs(v)) if v.size and not np.isnan(v).all() else 0.0
             tol = torch.finfo(self.dtype).eps / 2 * abs(wo) + (2 * ds + 2.0 ** -20) * mag + 1e-30
             if bf:

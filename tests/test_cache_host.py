@@ -49,7 +49,7 @@ def test_cache_sizes():
     (dict(B=0), 1), (dict(T=-1), 1), (dict(Hq=7), 1), (dict(page_size=24), 1),
     (dict(page_size=0), 1), (dict(pages=0), 1), (dict(max_pages=0), 1), (dict(window=-1), 1),
     (dict(window=5, causal=False), 1), (dict(scale=float("nan")), 1), (dict(dtype=9), 1),
-    (dict(max_q=-1), 1), (dict(scale=1e300), 1),
+    (dict(max_q=-1), 1), (dict(scale=1e300), 1), (dict(scale=-0.1), 1),
     (dict(d=96), 2), (dict(d=256), 2), (dict(page_size=8192), 2), (dict(B=65537), 2),
     (dict(Hq=8192, Hkv=2), 2), (dict(max_pages=1 << 30), 2), (dict(T=1 << 40), 2),
     (dict(T=1 << 30, Hq=4096, Hkv=2), 2), (dict(pages=1 << 40), 2),
@@ -181,8 +181,9 @@ def fake(monkeypatch):
     f = FakeLib()
     monkeypatch.setattr(rb, "lib", lambda: f)
     monkeypatch.setattr(rb, "_stream", lambda device: ctypes.c_void_p(0))
-    monkeypatch.setattr(rb, "_serving_device", lambda fn, t: t.device)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(rb, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(rb, "_serving_device", lambda fn, t: t.get_device())   # -1: host memory
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
     return f
 
 
@@ -238,7 +239,7 @@ def test_malformed_serving_tensors_are_refused_before_any_call(fake):
         lambda: rb.rope_attn_cache_attn(*with_(2, t["table"].long()), t["q"], ws=t["ws"]),
         lambda: rb.rope_attn_cache_attn(*with_(2, t["table"][:, :3]), t["q"], ws=t["ws"]),
         lambda: rb.rope_attn_cache_attn(*with_(3, t["indptr"][:2]), t["q"], ws=t["ws"]),
-        lambda: rb.rope_attn_cache_attn(*with_(4, t["kv_len"].to("meta")), t["q"], ws=t["ws"]),
+        lambda: rb.rope_attn_cache_attn(*with_(4, t["kv_len"][:1]), t["q"], ws=t["ws"]),
         lambda: rb.rope_attn_cache_attn(*head, t["q"], o=t["q"][:, :4], ws=t["ws"]),
         lambda: rb.rope_attn_cache_append(*head, spec, f, t["kv"], t["q"], ws=t["ws"]),
         lambda: rb.rope_attn_cache_append(*head, spec, f.float(), t["kv"], t["kv"], ws=t["ws"]),

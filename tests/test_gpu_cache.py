@@ -102,6 +102,17 @@ def test_query_strides(dtype):
     assert torch.equal(o, o2) and torch.equal(lse, l2)
 
 
+def test_host_tensors_are_refused():
+    b = Batch([(1, 40)], 4, 2, 64, 16, "bf16").device()
+    for i in range(1, 5):
+        head = list(b.head)
+        head[i] = head[i].cpu()
+        with pytest.raises(ValueError):
+            rb.rope_attn_cache_attn(*head, b.c["q"], ws=b.c["ws"])
+    with pytest.raises(ValueError):
+        rb.rope_attn_cache_attn(*b.head, b.c["q"].cpu(), ws=b.c["ws"])
+
+
 def test_scale_is_taken():
     b = Batch([(1, 100), (70, 90)], 4, 2, 64, 16, "bf16", scale=0.05).device()
     b.check(*b.attn())
