@@ -632,8 +632,8 @@ def rope_attn_cache_read(plan, cache, table, indptr, kv_len, k=None, v=None, ws=
     fn = "rope_attn_cache_read"
     dev, head, tail, dt = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)
     kv = (plan.T, plan.Hkv, plan.d)
-    k = torch.empty(kv, dtype=dt, device=cache.device) if k is None else k
-    v = torch.empty(kv, dtype=dt, device=cache.device) if v is None else v
+    k = cache.new_empty(kv, dtype=dt) if k is None else k
+    v = cache.new_empty(kv, dtype=dt) if v is None else v
     rows = [_head_rows(fn, "k", k, dev, dt, kv), _head_rows(fn, "v", v, dev, dt, kv)]
     _call(fn, dev, *head, ctypes.byref(rows[0]), ctypes.byref(rows[1]), *tail)
     return k, v
@@ -647,8 +647,8 @@ def rope_attn_cache_attn(plan, cache, table, indptr, kv_len, q, o=None, lse=None
     T, Hq = plan.T, plan.Hq
     qs = (T, Hq, plan.d)
     rows = _head_rows(fn, "q", q, dev, dt, qs)
-    o = torch.empty(qs, dtype=dt, device=q.device) if o is None else o
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
+    o = q.new_empty(qs) if o is None else o
+    lse = q.new_empty((T, Hq), dtype=torch.float32) if lse is None else lse
     _call(fn, dev, *head, ctypes.byref(rows), _vector(fn, "o", o, dev, dt, qs),
           _vector(fn, "lse", lse, dev, torch.float32, (T, Hq)), *tail)
     return o, lse

@@ -220,26 +220,87 @@ __global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const AttnA
 }
 
 // ------------------------------------------------------------------ joining split items
-// Block (c, r): row r (and every gridDim.y-th after it) of the split item that begins in block
-// c of the attention launch.  8 warps share the parts, a lane D / 32 channels.
-constexpr int kCombineThreads = 256;
+// Block x joins the split item that begins in block x of an attention launch (of the first
+// launch's blocks, then of the second's).  Few parts: a warp takes a row, blockIdx.y and the
+// block's warps share the rows.  Many parts (one long cache over most of the GPU, few rows): the
+// block takes a row, its warps share the parts.
+constexpr int kCombineThreads = 256, kCombineWarps = kCombineThreads / 32;
+constexpr int kWarpParts = 16;  // most parts that one warp walks alone
+
+struct CombineArgs {
+  AttnArgs a[2];
+  int blocks[2];  // 0: no such launch
+};
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kCombineThreads) cache_combine_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kCombineThreads)
+    cache_combine_kernel(const __grid_constant__ CombineArgs ca) {
   constexpr int DL = D / 32;
-  __shared__ float red[8][D], red_l[8];
-  __shared__ float mx_s[8];
+  __shared__ float red[kCombineWarps][D], red_l[kCombineWarps], mx_s[kCombineWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const PartDesc d = a.desc[blockIdx.x];
+  const int which = (int)blockIdx.x < ca.blocks[0] ? 0 : 1;
+  const AttnArgs& a = ca.a[which];
+  const int first = blockIdx.x - (which ? ca.blocks[0] : 0);
+  const PartDesc d = a.desc[first];
   if (d.followers == 0) return;
   const CacheDims& c = a.c;
   const int G = c.Hq / c.Hkv, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const SeqWork w = load_work(a, d.b);
-  const long long row0 = (long long)d.tile * a.tile;
-  const int rows = (int)min((long long)a.tile, (long long)w.qn * G - row0);
   const int parts = d.followers + 1;
-  // part 0 is the beginning block's "goes on" slot, part k > 0 block c + k's "came over" slot
-  auto slot_of = [&](int k) { return 2ll * (blockIdx.x + k) + (k == 0 ? 1 : 0); };
+  const int q0 = a.indptr[d.b], q1 = a.indptr[d.b + 1];
+  const long long row0 = (long long)d.tile * a.tile;
+  const int rows = (int)min((long long)a.tile, (long long)(q1 - q0) * G - row0);
+  // part 0 is the beginning block's "goes on" slot, part k > 0 block first + k's "came over" slot
+  auto slot_of = [&](int k) { return 2ll * (first + k) + (k == 0 ? 1 : 0); };
+  auto write = [&](int r, int ch, const float* x, int n, float mx, float l) {
+    const long long row = row0 + r, token = row / G;
+    const long long at = (q0 + token) * c.Hq + (long long)d.h * G + (row - token * G);
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int e = 0; e < DL; ++e) {
+      if (e >= n) break;
+      Vec<T, 1> v;
+      const float f[1] = {x[e] * inv};
+      v.set(f);
+      v.store(static_cast<T*>(a.o) + at * D + ch + e);
+    }
+    if (ch == 0) a.lse[at] = (mx + log2f(l)) * 0.6931471805599453f;
+  };
+  if (parts <= kWarpParts) {
+    for (int r = blockIdx.y * kCombineWarps + warp; r < rows; r += gridDim.y * kCombineWarps) {
+      float m = -CUDART_INF_F, l = 0.f;
+      if (lane < parts) {
+        m = a.ml[(slot_of(lane) * a.tile + r) * 2];
+        l = a.ml[(slot_of(lane) * a.tile + r) * 2 + 1];
+      }
+      float mx = m;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float f = m == -CUDART_INF_F ? 0.f : exp2f(m - mx);
+      l *= f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      float acc[DL];
+#pragma unroll
+      for (int e = 0; e < DL; ++e) acc[e] = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < parts; ++k) {
+        const float w = __shfl_sync(0xffffffffu, f, k);
+        const float* src = a.acc + (slot_of(k) * a.tile + r) * D + lane * DL;
+        float x[DL];
+        if constexpr (DL == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          x[0] = v.x, x[1] = v.y;
+        }
+#pragma unroll
+        for (int e = 0; e < DL; ++e) acc[e] = fmaf(w, x[e], acc[e]);
+      }
+      write(r, lane * DL, acc, DL, mx, l);
+    }
+    return;
+  }
   for (int r = blockIdx.y; r < rows; r += gridDim.y) {
     float mx = -CUDART_INF_F;
     for (int k = threadIdx.x; k < parts; k += kCombineThreads)
@@ -249,13 +310,13 @@ __global__ void __launch_bounds__(kCombineThreads) cache_combine_kernel(const At
     if (lane == 0) mx_s[warp] = mx;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 8; ++k) mx = fmaxf(mx, mx_s[k]);
+    for (int k = 0; k < kCombineWarps; ++k) mx = fmaxf(mx, mx_s[k]);
     float acc[DL], l = 0.f;
 #pragma unroll
     for (int e = 0; e < DL; ++e) acc[e] = 0.f;
     if (mx != -CUDART_INF_F) {
-#pragma unroll 4
-      for (int k = warp; k < parts; k += 8) {
+#pragma unroll 8
+      for (int k = warp; k < parts; k += kCombineWarps) {
         const long long at = slot_of(k) * a.tile + r;
         const float f = exp2f(a.ml[at * 2] - mx);
         l = fmaf(f, a.ml[at * 2 + 1], l);
@@ -271,17 +332,11 @@ __global__ void __launch_bounds__(kCombineThreads) cache_combine_kernel(const At
     if (threadIdx.x < D) {
       float sum = 0.f, wl = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < kCombineWarps; ++k) {
         sum += red[k][threadIdx.x];
         wl += red_l[k];
       }
-      const long long row = row0 + r;
-      const long long at = (w.q0 + row / G) * c.Hq + (long long)d.h * G + row % G;
-      Vec<T, 1> v;
-      const float f[1] = {wl > 0.f ? sum / wl : 0.f};
-      v.set(f);
-      v.store(static_cast<T*>(a.o) + at * D + threadIdx.x);
-      if (threadIdx.x == 0) a.lse[at] = (mx + log2f(wl)) * 0.6931471805599453f;
+      write(r, threadIdx.x, &sum, 1, mx, wl);
     }
     __syncthreads();
   }
@@ -308,12 +363,15 @@ cudaError_t launch_f32(AttnArgs& a, int rows, cudaStream_t s) {
 
 }  // namespace
 
+namespace {
+
 // The combine launch overlaps its start with the attention kernel's end (programmatic stream
-// serialisation: it waits for that kernel's writes before it reads any).
-cudaError_t launch_cache_combine(const AttnArgs& a, int blocks, int32_t dtype, int rows,
-                                 cudaStream_t s) {
+// serialisation: it waits for that kernel's writes before it reads any).  rows: most rows of
+// an item.
+cudaError_t launch_combine(const CombineArgs& ca, int32_t dtype, int d, int rows,
+                           cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)blocks, (unsigned)std::min(rows, 64));
+  cfg.gridDim = dim3((unsigned)(ca.blocks[0] + ca.blocks[1]), (unsigned)std::min(rows, 32));
   cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -322,12 +380,13 @@ cudaError_t launch_cache_combine(const AttnArgs& a, int blocks, int32_t dtype, i
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if (dtype == RA_BF16)
-    return a.c.d == 64 ? cudaLaunchKernelEx(&cfg, cache_combine_kernel<__nv_bfloat16, 64>, a)
-                       : cudaLaunchKernelEx(&cfg, cache_combine_kernel<__nv_bfloat16, 128>, a);
-  return a.c.d == 64 ? cudaLaunchKernelEx(&cfg, cache_combine_kernel<float, 64>, a)
-                     : cudaLaunchKernelEx(&cfg, cache_combine_kernel<float, 128>, a);
+    return d == 64 ? cudaLaunchKernelEx(&cfg, cache_combine_kernel<__nv_bfloat16, 64>, ca)
+                   : cudaLaunchKernelEx(&cfg, cache_combine_kernel<__nv_bfloat16, 128>, ca);
+  return d == 64 ? cudaLaunchKernelEx(&cfg, cache_combine_kernel<float, 64>, ca)
+                 : cudaLaunchKernelEx(&cfg, cache_combine_kernel<float, 128>, ca);
 }
 
+}  // namespace
 }  // namespace ra
 
 using namespace ra;
@@ -336,10 +395,10 @@ extern "C" {
 
 size_t rope_attn_cache_workspace_bytes(const ra_cache* p) {
   if (check_cache(p) != RA_OK) return 0;
-  const size_t rows = cache_ws(kRowsBlocks, kRowsTile, (int)p->d).total;
-  const int64_t most = cache_dims(*p).max_q * (p->Hq / p->Hkv);
-  if (p->dtype != RA_BF16 || most <= kChunkMinRows) return rows;
-  return std::max(rows, cache_ws(kChunkBlocks, kChunkTile, (int)p->d).total);
+  size_t total = cache_ws(kCacheErrBytes, kRowsBlocks, kRowsTile, (int)p->d).total;
+  if (p->dtype == RA_BF16 && (int64_t)cache_dims(*p).max_q * (p->Hq / p->Hkv) > kChunkMinRows)
+    total = cache_ws(total, kChunkBlocks, kChunkTile, (int)p->d).total;
+  return total;
 }
 
 ra_status rope_attn_cache_attn(const ra_cache* p, const void* cache, const int32_t* table,
@@ -367,47 +426,43 @@ ra_status rope_attn_cache_attn(const ra_cache* p, const void* cache, const int32
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t most_rows = (int64_t)a.c.max_q * (p->Hq / p->Hkv);  // of one sequence and head
 
-  // One kernel and the combine of what it split; the workspace after the error word is its own
-  // until the combine has read it.
-  auto partials = [&](int blocks, int tile) {
-    const CacheWs w = cache_ws(blocks, tile, a.c.d);
-    a.desc = reinterpret_cast<PartDesc*>(base + w.desc);
-    a.ml = reinterpret_cast<float*>(base + w.ml);
-    a.acc = reinterpret_cast<float*>(base + w.acc);
-  };
-  auto combine = [&](int blocks, int64_t rows) {
-    const TimingScope timed(K_CACHE_COMBINE, s);
-    return launch_cache_combine(a, blocks, p->dtype, (int)std::min<int64_t>(rows, a.tile), s);
+  CombineArgs ca{};
+  // the launch's own region of the workspace, from `at` on
+  auto partials = [&](AttnArgs& x, size_t at, int blocks, int tile) {
+    const CacheWs w = cache_ws(at, blocks, tile, x.c.d);
+    x.desc = reinterpret_cast<PartDesc*>(base + w.desc);
+    x.ml = reinterpret_cast<float*>(base + w.ml);
+    x.acc = reinterpret_cast<float*>(base + w.acc);
+    return w.total;
   };
   cudaError_t e;
-  int blocks = kRowsBlocks;
   a.min_rows = 0, a.max_rows = int64_t(1) << 62;
   a.min_steps = 2;
-  partials(kRowsBlocks, kRowsTile);
+  const size_t rows_end = partials(a, kCacheErrBytes, kRowsBlocks, kRowsTile);
   if (p->dtype == RA_F32) {
-    {
-      const TimingScope timed(K_CACHE_ATTN_F32, s);
-      const int rows = (int)std::min<int64_t>(most_rows, 8);
-      e = p->d == 64 ? launch_f32<64>(a, rows, s) : launch_f32<128>(a, rows, s);
-    }
-    if (e == cudaSuccess) e = combine(blocks, most_rows);
-    return e == cudaSuccess ? RA_OK : RA_ERR_CUDA;
-  }
-  a.max_rows = kChunkMinRows;
-  {
+    const TimingScope timed(K_CACHE_ATTN_F32, s);
+    const int rows = (int)std::min<int64_t>(most_rows, 8);
+    ca.blocks[0] = kRowsBlocks;
+    e = p->d == 64 ? launch_f32<64>(a, rows, s) : launch_f32<128>(a, rows, s);
+  } else {
+    // every sequence goes to the kernel for its own number of rows, whatever the others have
+    a.max_rows = kChunkMinRows;
     const TimingScope timed(K_CACHE_ATTN, s);
-    e = launch_cache_rows(a, std::min<int64_t>(most_rows, kChunkMinRows), &blocks, s);
+    e = launch_cache_rows(a, std::min<int64_t>(most_rows, kChunkMinRows), &ca.blocks[0], s);
   }
-  if (e == cudaSuccess) e = combine(blocks, most_rows);
-  if (e == cudaSuccess && most_rows > kChunkMinRows) {
+  ca.a[0] = a;
+  if (e == cudaSuccess && p->dtype == RA_BF16 && most_rows > kChunkMinRows) {
     a.min_rows = kChunkMinRows, a.max_rows = int64_t(1) << 62;
     a.min_steps = 1;
-    partials(kChunkBlocks, kChunkTile);
-    {
-      const TimingScope timed(K_CACHE_ATTN_CHUNK, s);
-      e = launch_cache_chunk(a, s);
-    }
-    if (e == cudaSuccess) e = combine(kChunkBlocks, most_rows);
+    partials(a, rows_end, kChunkBlocks, kChunkTile);
+    ca.blocks[1] = kChunkBlocks;
+    const TimingScope timed(K_CACHE_ATTN_CHUNK, s);
+    e = launch_cache_chunk(a, s);
+    ca.a[1] = a;
+  }
+  if (e == cudaSuccess) {
+    const TimingScope timed(K_CACHE_COMBINE, s);
+    e = launch_combine(ca, p->dtype, a.c.d, (int)std::min<int64_t>(most_rows, a.tile), s);
   }
   return e == cudaSuccess ? RA_OK : RA_ERR_CUDA;
 }

@@ -13,7 +13,4 @@ struct AttnArgs;
 cudaError_t launch_cache_rows(AttnArgs& a, long long rows, int* blocks, cudaStream_t s);
 // bf16, sequences of many rows: kChunkBlocks blocks, tiles of kChunkTile rows.
 cudaError_t launch_cache_chunk(AttnArgs& a, cudaStream_t s);
-cudaError_t launch_cache_combine(const AttnArgs& a, int blocks, int32_t dtype, int rows,
-                                 cudaStream_t s);
-
 }  // namespace ra

@@ -30,6 +30,8 @@
 #include <cuda_fp16.h>
 #include <math_constants.h>
 
+#include <atomic>
+
 #include "cache_attn.h"
 #include "cache_sched.cuh"
 #include "common.h"
@@ -552,8 +554,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const Att
 template <int D>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   using C = ChunkCfg<D>;
-  const cudaError_t e = cudaFuncSetAttribute(
-      cache_attn_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  // once per device: a decode step is short against the call
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && !(dev < 64 && done.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(cache_attn_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::SMEM);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev);
+  }
   if (e != cudaSuccess) return e;
   cache_attn_chunk_kernel<D><<<kChunkBlocks, kThreads, C::SMEM, s>>>(a);
   return cudaGetLastError();

@@ -9,25 +9,34 @@
 //     blocks into a private ring of shared memory (one cp.async.bulk per block, its own
 //     mbarriers) and keeps its own online softmax.  The four warps of a block meet only at the
 //     end of an item.
+//   * A code never becomes its value.  Or-ing four bits into the mantissa of an fp16 constant
+//     gives 1024 + c (bits 0-3) or 64 + c (bits 4-7): a word of eight codes is four operand
+//     registers for one shift and four logic operations.  What the biases and the (step, lo)
+//     pairs add is linear and comes in outside the inner products:
 //   * S^T = K Q^T with mma.sync.m16n8k16: 16 keys are the M rows, the (up to 8 per tile) query
-//     rows the N columns.  A code c becomes the bf16 value 128 + c by or-ing it under that
-//     exponent: one shift and one three-input logic operation per two codes, and the products
-//     with the bf16 queries are exact.  The pair of a key and group comes in afterwards, on the
-//     accumulators: s = step acc + (lo - 128 step) sum(q), 4 FMAs per 128 codes instead of one
-//     per two.
-//   * P V as O^T = V^T P^T: channels are the M rows, so that P^T is the B operand; movmatrix
-//     turns the fp16 score tile around in registers.  Codes of two keys are interleaved with
-//     one permute and become fp16 1024 + c the same way; subtracting 1024 and one packed FMA
-//     give lo + step c, rounded once to fp16 (11 bits: the scores' weights P are fp16 too).
+//     rows the N columns.  The accumulator starts at minus the bias times sum(q), which leaves
+//     q . c exactly; then s = step acc + lo sum(q), per key and group.
+//   * P V as O^T = V^T P^T: channels are the M rows, P^T the B operand, scaled by the keys' steps
+//     before it is rounded to fp16 (one copy per group of 64 channels) and turned around in
+//     registers by movmatrix.  The bias is the same multiple of sum(p step) for every channel:
+//     one more product with ones gives that sum as it was rounded, and every kFlush shares it is
+//     taken off the accumulators, before the tensor cores' fp32 sums (which need not round to
+//     nearest) could lose bits to it.  8 more steps are taken off with it and come back in fp32
+//     with the low ends, sum(p (lo + 8 step)): the rounding of p step then multiplies codes
+//     of -8 .. 7 instead of 0 .. 15.
 //   * Which key or channel sits in which MMA row is free as long as both products agree; it is
 //     chosen so that every shared-memory read is a conflict-free or two-way 4- or 8-byte
 //     access of the cache's plain channel order.
+//   * Weights stay below 2^kTau = 4, and a step is at most 2 RA_CACHE_LIMIT / 15 = 8000, so
+//     p step stays inside fp16.  Queries enter as fp16 (clamped and reported beyond 65504).
 //
 // mma.sync rather than tcgen05: with at most 16 query rows the tensor work is a fraction of
 // what mma.sync sustains, and its operands come straight from registers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
+
+#include <atomic>
 
 #include "cache_attn.h"
 #include "cache_sched.cuh"
@@ -39,12 +48,15 @@ namespace ra {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kStages = 2;             // ring of a warp, in its 32-token shares of a step
-constexpr float kTau = 8.0f;           // lazy rescale of the running max, log2 units
+constexpr int kStages = 3;             // ring of a warp, in its 32-token shares of a step
+constexpr float kTau = 2.0f;           // lazy rescale of the running max, log2 units
+constexpr int kFlush = 16;             // shares between two removals of the codes' bias
+constexpr float kBiasEven = 1024.f, kBiasOdd = 64.f, kMid = 8.f;
+constexpr uint32_t kEvenBits = 0x64006400u, kOddBits = 0x54005400u;  // those as fp16 pairs
 
 template <int D, int NT>
 struct RowsCfg {
-  static constexpr int CTAS = NT == 1 ? 4 : 3;              // per SM
+  static constexpr int CTAS = NT == 2 ? 2 : D == 64 ? 4 : 3;              // per SM
   static constexpr int BLOCK_BYTES = block_bytes(D);
   static constexpr int STAGE = 2 * BLOCK_BYTES;
   static constexpr int RING = kStages * STAGE;              // per warp
@@ -53,24 +65,18 @@ struct RowsCfg {
   static constexpr int OFF_ML = OFF_MERGE + kWarps * 32 * NACC * 4;
   static constexpr int OFF_BAR = OFF_ML + kWarps * NT * 8 * 2 * 4;
   static constexpr int OFF_SCRATCH = OFF_BAR + kWarps * kStages * 8;
-  static constexpr int SMEM = OFF_SCRATCH + 8 * (kWarps + 4);
+  static constexpr int OFF_WALK = OFF_SCRATCH + 8 * (kWarps + 4);
+  static constexpr int SMEM = OFF_WALK + (int)sizeof(SharedWalk);
 };
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
+                                        float c2, float c3) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 // The 8 x 8 matrix of 16-bit elements held by the warp (lane: row lane / 4, columns
 // 2 (lane % 4), + 1) transposed.
@@ -98,19 +104,18 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
 
-// Codes of four channels of two keys -> their values in fp16, (key a, key b) pairs:
-// x holds the four nibbles of key a in its low and of key b in its high half.
-__device__ __forceinline__ void values4(uint32_t x, __half2 step, __half2 lo, uint32_t* v) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 c = as_half2(and_or(x >> (4 * i), 0x000f000fu, 0x64006400u));
-    v[i] = as_u32(__hfma2(__hsub2(c, as_half2(0x64006400u)), step, lo));
-  }
+// The A registers of two channels: even one 1024 + c, odd one 64 + c, from the low eight bits of
+// each half of x.
+__device__ __forceinline__ uint32_t even_codes(uint32_t x) {
+  return and_or(x, 0x000f000fu, kEvenBits);
+}
+__device__ __forceinline__ uint32_t odd_codes(uint32_t x) {
+  return and_or(x, 0x00f000f0u, kOddBits);
 }
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
-    cache_attn_rows_kernel(const AttnArgs a) {
+    cache_attn_rows_kernel(const __grid_constant__ AttnArgs a) {
   using C = RowsCfg<D, NT>;
   constexpr int NG = D / kGroup;     // groups of a row
   constexpr int TILE = 8 * NT;       // query rows
@@ -131,10 +136,14 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
     fence_barrier_init();
   }
   __syncwarp();
-  const Run run = find_run(a, reinterpret_cast<long long*>(smem + C::OFF_SCRATCH), K_CACHE_ATTN);
-  Walk<WorkOf> walk(WorkOf{a}, run, c.B);
-  Segment s;
-  int followers = 0, fb = 0, fh = 0, ft = 0;
+  SharedWalk& walk = *reinterpret_cast<SharedWalk*>(smem + C::OFF_WALK);
+  {
+    const Run run =
+        find_run(a, reinterpret_cast<long long*>(smem + C::OFF_SCRATCH), K_CACHE_ATTN);
+    if (threadIdx.x == 0) walk.start(a, run);
+    __syncthreads();
+  }
+  PartDesc split{0, 0, 0, 0};
   uint32_t issued = 0, consumed = 0;  // shares of this warp so far: stage = n % kStages
   int gave_up = 0;                    // a bounded wait expired: no more copies, no more waits
 
@@ -142,80 +151,76 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
   // owns keys t, t + 4, t + 8, t + 12
   const int krow = (r & 1) * 4 + (r >> 1);
 
-  while (walk.next(s)) {
-    const long long row0 = (long long)s.tile * TILE;
-    const int rows = (int)min((long long)TILE, (long long)s.w.qn * G - row0);
-    // keys that the lane's query columns (8 nt + 2 t, + 1) see; the tile's first and last rows
-    // bound those of all (both ends rise with the row)
-    int q_lo[NT][2], q_hi[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int n = 8 * nt + 2 * t + e;
-        const KeyRange k = n < rows ? row_keys(c, s.w, row0 + n, G) : KeyRange{0, 0};
-        q_lo[nt][e] = k.lo;
-        q_hi[nt][e] = k.hi;
+  // ---- the current segment as its copies need it: this warp's shares [i0, i1) of its steps
+  // that hold a visible key, share 0 beginning at key `base`
+  int base = 0, L = 0, i0 = 0, i1 = 0, next = 0;
+  // Lane l keeps the address of block l % 2 of share ad_base + l / 2 (null behind the last
+  // token or where the table is bad) and copies that block itself when its turn comes.
+  const uint8_t* ad = nullptr;
+  int ad_base = 0;
+  uint32_t good = 0;     // the lanes that have an address
+  uint32_t present = 0;  // bits 2 stage + block: the stage's block was copied
+  auto issue = [&](const Segment& s, int i) {
+    if (i - ad_base >= 16) {
+      ad_base = i;
+      const int share = i + lane / 2, blk = (base + share * kStep) / kBlock + lane % 2;
+      ad = nullptr;
+      if (share < i1 && blk * kBlock < L) {
+        const int page = page_of(c, a.table, s.b, blk, a.err, K_CACHE_ATTN);
+        if (page >= 0) ad = a.cache + block_at(c, page, s.h, blk % c.page_blocks);
       }
-    const KeyRange kf = row_keys(c, s.w, row0, G), kl = row_keys(c, s.w, row0 + rows - 1, G);
-    // this warp's shares of the segment's steps that hold a visible key: [i0, i1)
-    const int base = s.key0 + warp * 32;   // key of share 0
-    int i0 = s.s0, i1 = s.s1;
+      good = __ballot_sync(0xffffffffu, ad != nullptr);
+    }
+    const int stage = issued % kStages, mine = lane - 2 * (i - ad_base);
+    ++issued;
+    const uint32_t have = good >> (2 * (i - ad_base)) & 3u;
+    present = (present & ~(3u << (2 * stage))) | have << (2 * stage);
+    if (mine == 0) mbar_arrive_expect_tx(&bar[stage], __popc(have) * C::BLOCK_BYTES);
+    if ((mine & ~1) == 0 && ad)
+      bulk_load(ring + stage * C::STAGE + mine * C::BLOCK_BYTES, ad, C::BLOCK_BYTES,
+                &bar[stage]);
+  };
+  // take up segment s and begin its copies (the ring is empty)
+  auto begin = [&](const Segment& s) {
+    const int row0 = s.tile * TILE, rows = min(TILE, s.w.qn * G - row0);
+    const KeyRange kf = token_keys(c, s.w, row0 / G);
+    const KeyRange kl = token_keys(c, s.w, (row0 + rows - 1) / G);
+    base = s.key0 + warp * 32;
+    L = s.w.L;
+    i0 = s.s0, i1 = s.s1;
     if (kl.hi <= base) i1 = i0;
     else i1 = min(i1, (kl.hi - base + kStep - 1) / kStep);
     if (kf.lo >= base + 32) i0 = max(i0, (kf.lo - base - 32) / kStep + 1);
+    ad_base = i0 - 64;
+    for (next = i0; next < i1 && next < i0 + kStages && !gave_up; ++next) issue(s, next);
+  };
 
-    // pages of the two blocks of 16 shares from `pg_base`: lane l holds block l % 2 of share
-    // pg_base + l / 2; -1 behind the last token or where the table is bad
-    int pg = -1, pg_base = i0 - 64;
-    uint32_t present = 0;  // bits 2 stage + block: the stage's block was copied
-    auto issue = [&](int i) {
-      if (i - pg_base >= 16) {
-        pg_base = i;
-        const int key = base + (i + lane / 2) * kStep + (lane % 2) * kBlock;
-        pg = -1;
-        if (i + lane / 2 < i1 && key < s.w.L)
-          pg = page_of(c, a.table, s.b, key / kBlock, a.err, K_CACHE_ATTN);
-      }
-      const int stage = issued % kStages;
-      ++issued;
-      uint32_t have = 0;
-      int page[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        page[k] = __shfl_sync(0xffffffffu, pg, 2 * (i - pg_base) + k);
-        have |= page[k] >= 0 ? 1u << k : 0u;
-      }
-      present = (present & ~(3u << (2 * stage))) | have << (2 * stage);
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bar[stage], __popc(have) * C::BLOCK_BYTES);
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (page[k] >= 0) {
-            const int blk = (base + i * kStep) / kBlock + k;
-            bulk_load(ring + stage * C::STAGE + k * C::BLOCK_BYTES,
-                      a.cache + block_at(c, page[k], s.h, blk % c.page_blocks), C::BLOCK_BYTES,
-                      &bar[stage]);
-          }
-      }
-    };
-    int next = i0;
-    for (; next < i1 && next < i0 + kStages && !gave_up; ++next) issue(next);
+  if (walk.more[0]) begin(walk.seg[0]);
+  for (int sg = 0; walk.more[sg % 2]; ++sg) {
+    const Segment& s = walk.seg[sg % 2];
+    if (threadIdx.x == kThreads - 32) walk.advance(sg + 1);
+    // at most kChunkMinRows rows
+    const int row0 = s.tile * TILE, rows = min(TILE, s.w.qn * G - row0);
+    // the tile's first and last rows bound what all see (both ends rise with the row): a share
+    // between the last one's begin and the first one's end needs no mask
+    const int lo_most = token_keys(c, s.w, (row0 + rows - 1) / G).lo;
+    const int hi_least = token_keys(c, s.w, row0 / G).hi;
 
     // queries as B operands (row n = 8 nt + lane / 4): the channel pairs (i, i + 4) of each
-    // eight, as the codes are unpacked; and their sums over each group
+    // eight, as the codes are unpacked; their sums over each group, plain and times the bias
     uint32_t qb[NT][NG][8];
-    float qs[NT][NG][2];
+    float2 qs[NT][NG];
+    float qbias[NT][NG][4];  // as an accumulator's four elements
+    bool beyond = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int n = 8 * nt + r;
-      const long long row = row0 + n;
+      const int token = (row0 + n) / G, hd = s.h * G + (row0 + n) - token * G;
       const __nv_bfloat16* src =
-          static_cast<const __nv_bfloat16*>(a.q) + (s.w.q0 + row / G) * a.q_n +
-          ((long long)s.h * G + row % G) * a.q_h;
+          static_cast<const __nv_bfloat16*>(a.q) + (s.w.q0 + token) * a.q_n + hd * a.q_h;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        float sum = 0.f;
+        float even = 0.f, odd = 0.f;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -230,31 +235,72 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
               for (int e = 0; e < 4; ++e) w[e] = h[2 * e] | ((uint32_t)h[2 * e + 1] << 16);
             }
           }
+          float f[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            sum += __uint_as_float(w[e] << 16) + __uint_as_float(w[e] & 0xffff0000u);
-          qb[nt][g][4 * j + 0] = __byte_perm(w[0], w[2], 0x5410);
-          qb[nt][g][4 * j + 1] = __byte_perm(w[0], w[2], 0x7632);
-          qb[nt][g][4 * j + 2] = __byte_perm(w[1], w[3], 0x5410);
-          qb[nt][g][4 * j + 3] = __byte_perm(w[1], w[3], 0x7632);
+          for (int e = 0; e < 4; ++e) {
+            f[2 * e] = __uint_as_float(w[e] << 16);
+            f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) beyond = beyond || !(fabsf(f[e]) <= 65504.f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t x = pack_f16x2_sat(f[e], f[e + 4]);
+            const float2 y = __half22float2(as_half2(x));  // as rounded
+            qb[nt][g][4 * j + e] = x;
+            if (e % 2 == 0) even += y.x + y.y;
+            else odd += y.x + y.y;
+          }
         }
+        float sum = even + odd, bias = kBiasEven * even + kBiasOdd * odd;
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qs[nt][g][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
-        qs[nt][g][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+        bias += __shfl_xor_sync(0xffffffffu, bias, 1);
+        bias += __shfl_xor_sync(0xffffffffu, bias, 2);
+        qs[nt][g] = make_float2(__shfl_sync(0xffffffffu, sum, 8 * t),
+                                __shfl_sync(0xffffffffu, sum, 8 * t + 4));
+        qbias[nt][g][0] = qbias[nt][g][2] = -__shfl_sync(0xffffffffu, bias, 8 * t);
+        qbias[nt][g][1] = qbias[nt][g][3] = -__shfl_sync(0xffffffffu, bias, 8 * t + 4);
       }
     }
+    if (beyond) atomicCAS(a.err, 0u, (uint32_t)RA_ERR_RANGE);
 
-    float m[NT][2], l[NT][2], o[NT][MT][4];
+    // running maximum (log2 units), sums of p, O; sums of p step as rounded since the last
+    // flush, and of p (lo + 8 step)
+    float m2[NT][2], o[NT][MT][4], ones[NT][NG][4];
+    float2 l[NT], plo[NT][NG];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      m2[nt][0] = m2[nt][1] = -CUDART_INF_F;
+      l[nt] = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) m[nt][e] = -CUDART_INF_F, l[nt][e] = 0.f;
+      for (int g = 0; g < NG; ++g) {
+        plo[nt][g] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ones[nt][g][e] = 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
     }
+    auto flush = [&]() {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float* x = o[nt][4 * g + i];
+            x[0] = fmaf(-kBiasEven - kMid, ones[nt][g][0], x[0]);
+            x[1] = fmaf(-kBiasEven - kMid, ones[nt][g][1], x[1]);
+            x[2] = fmaf(-kBiasOdd - kMid, ones[nt][g][0], x[2]);
+            x[3] = fmaf(-kBiasOdd - kMid, ones[nt][g][1], x[3]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ones[nt][g][e] = 0.f;
+        }
+    };
 
     for (int i = i0; i < i1; ++i) {
       if (gave_up) break;
@@ -268,175 +314,211 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
       const uint32_t have = present >> (2 * stage);
       const uint32_t st = ring_s + stage * C::STAGE;
       const int k0 = base + i * kStep;
-      // ---- scores, log2 units: rows krow, krow + 8 of each block; columns 2t, 2t + 1
-      float sc[2][NT][4];
+      // ---- scores: rows krow, krow + 8 of each block; columns 2 t, 2 t + 1
+      float2 sc[2][NT][2];  // [block][tile][row half]
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[k][nt][e] = 0.f;
-        if (!(have >> k & 1)) continue;
         const uint32_t kb = st + k * C::BLOCK_BYTES;
         const uint32_t pairs = kb + code_bytes(D);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           const uint2 wa = lds64(kb + krow * (D / 2) + g * 32 + t * 8);
           const uint2 wb = lds64(kb + (krow + 8) * (D / 2) + g * 32 + t * 8);
-          const float2 pa =
-              __half22float2(as_half2(lds32(pairs + (krow * NG + g) * 4)));
-          const float2 pb =
-              __half22float2(as_half2(lds32(pairs + ((krow + 8) * NG + g) * 4)));
+          const float2 pa = __half22float2(as_half2(lds32(pairs + (krow * NG + g) * 4)));
+          const float2 pb = __half22float2(as_half2(lds32(pairs + ((krow + 8) * NG + g) * 4)));
           float acc[NT][4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
-#pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t xa = j < 2 ? wa.x : wa.y, xb = j < 2 ? wb.x : wb.y;
-            const int sh = 8 * (j % 2);
-            const uint32_t a0 = and_or(xa >> sh, 0x000f000fu, 0x43004300u);
-            const uint32_t a1 = and_or(xb >> sh, 0x000f000fu, 0x43004300u);
-            const uint32_t a2 = and_or(xa >> (sh + 4), 0x000f000fu, 0x43004300u);
-            const uint32_t a3 = and_or(xb >> (sh + 4), 0x000f000fu, 0x43004300u);
+            uint32_t xa = j < 2 ? wa.x : wa.y, xb = j < 2 ? wb.x : wb.y;
+            if (j % 2) xa >>= 8, xb >>= 8;
+            const uint32_t a0 = even_codes(xa), a1 = even_codes(xb);
+            const uint32_t a2 = odd_codes(xa), a3 = odd_codes(xb);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_bf16(acc[nt], a0, a1, a2, a3, qb[nt][g][2 * j], qb[nt][g][2 * j + 1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              if (j == 0)
+                mma_f16(acc[nt], a0, a1, a2, a3, qb[nt][g][0], qb[nt][g][1], qbias[nt][g][0],
+                        qbias[nt][g][1], qbias[nt][g][2], qbias[nt][g][3]);
+              else
+                mma_f16(acc[nt], a0, a1, a2, a3, qb[nt][g][2 * j], qb[nt][g][2 * j + 1],
+                        acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+            }
           }
-          const float sa = pa.x * scale_log2, sb = pb.x * scale_log2;
-          const float oa = fmaf(-128.f, sa, pa.y * scale_log2);
-          const float ob = fmaf(-128.f, sb, pb.y * scale_log2);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            sc[k][nt][0] = fmaf(sa, acc[nt][0], fmaf(oa, qs[nt][g][0], sc[k][nt][0]));
-            sc[k][nt][1] = fmaf(sa, acc[nt][1], fmaf(oa, qs[nt][g][1], sc[k][nt][1]));
-            sc[k][nt][2] = fmaf(sb, acc[nt][2], fmaf(ob, qs[nt][g][0], sc[k][nt][2]));
-            sc[k][nt][3] = fmaf(sb, acc[nt][3], fmaf(ob, qs[nt][g][1], sc[k][nt][3]));
+            // scalar FMAs: the packed form would first have to double step and lo
+            float2 &x = sc[k][nt][0], &y = sc[k][nt][1];
+            x.x = fmaf(pa.x, acc[nt][0], g ? fmaf(pa.y, qs[nt][g].x, x.x) : pa.y * qs[nt][g].x);
+            x.y = fmaf(pa.x, acc[nt][1], g ? fmaf(pa.y, qs[nt][g].y, x.y) : pa.y * qs[nt][g].y);
+            y.x = fmaf(pb.x, acc[nt][2], g ? fmaf(pb.y, qs[nt][g].x, y.x) : pb.y * qs[nt][g].x);
+            y.y = fmaf(pb.x, acc[nt][3], g ? fmaf(pb.y, qs[nt][g].y, y.y) : pb.y * qs[nt][g].y);
           }
         }
       }
       // ---- mask: only where some row does not see the whole share
-      if (k0 + 32 > kf.hi || k0 < kl.lo || (have & 3) != 3) {
+      const bool partial = k0 + 32 > L || (have & 3) != 3;
+      if (partial || k0 + 32 > hi_least || k0 < lo_most) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int col = 0; col < 2; ++col) {
+            const int n = 8 * nt + 2 * t + col;
+            const KeyRange kr = n < rows ? token_keys(c, s.w, (row0 + n) / G) : KeyRange{0, 0};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = k0 + k * kBlock + krow + (e / 2) * 8;
-              if (!(have >> k & 1) || key < q_lo[nt][e % 2] || key >= q_hi[nt][e % 2])
-                sc[k][nt][e] = -CUDART_INF_F;
-            }
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int key = k0 + k * kBlock + krow + e * 8;
+                if (!(have >> k & 1) || key < kr.lo || key >= kr.hi)
+                  (col ? sc[k][nt][e].y : sc[k][nt][e].x) = -CUDART_INF_F;
+              }
+          }
       }
       // ---- running maximum of each column over the warp's eight row groups
       float mx[NT][2];
       bool grow = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        mx[nt][0] = fmaxf(fmax3(sc[0][nt][0].x, sc[0][nt][1].x, sc[1][nt][0].x), sc[1][nt][1].x);
+        mx[nt][1] = fmaxf(fmax3(sc[0][nt][0].y, sc[0][nt][1].y, sc[1][nt][0].y), sc[1][nt][1].y);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][e + 2]),
-                          fmaxf(sc[1][nt][e], sc[1][nt][e + 2]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          mx[nt][e] = x;
-          grow = grow || x > m[nt][e] + kTau;  // also the first finite maximum
+          mx[nt][e] *= scale_log2;
+          grow = grow || mx[nt][e] > m2[nt][e] + kTau;
         }
+      }
+      // the lanes' own maxima decide whether any column grows; only then are they joined
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float corr[2];
+          float2 corr;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float mn = fmaxf(m[nt][e], mx[nt][e]);
-            corr[e] = mn == -CUDART_INF_F ? 1.f : fast_exp2(m[nt][e] - mn);
-            m[nt][e] = mn;
-            l[nt][e] *= corr[e];
+            float x = mx[nt][e];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const float mn = fmaxf(m2[nt][e], x);
+            // nothing seen yet: the sums are 0
+            (e ? corr.y : corr.x) = mn == -CUDART_INF_F ? 0.f : fast_exp2(m2[nt][e] - mn);
+            m2[nt][e] = mn;
+          }
+          l[nt] = fmul2(l[nt], corr);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            plo[nt][g] = fmul2(plo[nt][g], corr);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ones[nt][g][e] *= e % 2 ? corr.y : corr.x;
           }
 #pragma unroll
-          for (int i2 = 0; i2 < MT; ++i2) {
-            o[nt][i2][0] *= corr[0];
-            o[nt][i2][1] *= corr[1];
-            o[nt][i2][2] *= corr[0];
-            o[nt][i2][3] *= corr[1];
-          }
+          for (int i2 = 0; i2 < MT; ++i2)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][i2][e] *= e % 2 ? corr.y : corr.x;
         }
       }
-      // ---- P = 2^(s - m) as fp16 B operands, and the values of each block
+      // ---- P = 2^(s - m); P step of each group as fp16 B operands; the codes of each block
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        uint32_t pb[NT][2];
+        const uint32_t vb = st + k * C::BLOCK_BYTES + value_offset(D);
+        const uint32_t pairs = vb + code_bytes(D);
+        float2 va[NG], vbp[NG];  // (step, lo + 8 step) of keys krow, krow + 8
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          va[g] = __half22float2(as_half2(lds32(pairs + (krow * NG + g) * 4)));
+          vbp[g] = __half22float2(as_half2(lds32(pairs + ((krow + 8) * NG + g) * 4)));
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          va[g].y = fmaf(kMid, va[g].x, va[g].y);
+          vbp[g].y = fmaf(kMid, vbp[g].x, vbp[g].y);
+        }
+        if (partial) {
+          // behind the last token, and in a block that was not copied, the pairs may be
+          // anything: 0 times them must be 0
+          const bool out = !(have >> k & 1);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            if (out || k0 + k * kBlock + krow >= L) va[g] = make_float2(0.f, 0.f);
+            if (out || k0 + k * kBlock + krow + 8 >= L) vbp[g] = make_float2(0.f, 0.f);
+          }
+        }
+        uint32_t pb[NT][NG][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float p[4];
+          const float2 nm = make_float2(m2[nt][0] == -CUDART_INF_F ? 0.f : -m2[nt][0],
+                                        m2[nt][1] == -CUDART_INF_F ? 0.f : -m2[nt][1]);
+          const float2 sl = make_float2(scale_log2, scale_log2);
+          const float2 ea = ffma2(sc[k][nt][0], sl, nm), eb = ffma2(sc[k][nt][1], sl, nm);
+          const float2 p0 = make_float2(fast_exp2(ea.x), fast_exp2(ea.y));
+          const float2 p1 = make_float2(fast_exp2(eb.x), fast_exp2(eb.y));
+          l[nt] = fadd2(l[nt], fadd2(p0, p1));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float mm = m[nt][e % 2] == -CUDART_INF_F ? 0.f : m[nt][e % 2];
-            p[e] = fast_exp2(sc[k][nt][e] - mm);
-          }
-          l[nt][0] += p[0] + p[2];
-          l[nt][1] += p[1] + p[3];
-          pb[nt][0] = transpose8(as_u32(__floats2half2_rn(p[0], p[1])));
-          pb[nt][1] = transpose8(as_u32(__floats2half2_rn(p[2], p[3])));
-        }
-        if (!(have >> k & 1)) continue;
-        const uint32_t vb = st + k * C::BLOCK_BYTES + value_offset(D);
-        const uint32_t pairs = vb + code_bytes(D) + (r * NG / 8) * 4;  // the lane's group
-        uint32_t pr[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          pr[e] = lds32(pairs + (t + 4 * e) * NG * 4);
-          // behind the last token the pairs may be anything: 0 times them must be 0
-          if (k0 + k * kBlock + t + 4 * e >= s.w.L) pr[e] = 0u;
-        }
-        const __half2 step01 = as_half2(__byte_perm(pr[0], pr[1], 0x5410)),
-                      lo01 = as_half2(__byte_perm(pr[0], pr[1], 0x7632)),
-                      step23 = as_half2(__byte_perm(pr[2], pr[3], 0x5410)),
-                      lo23 = as_half2(__byte_perm(pr[2], pr[3], 0x7632));
-        uint32_t w[4][D / 64];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t at = vb + (t + 4 * e) * (D / 2) + r * (D / 16);
-          if constexpr (D == 128) {
-            const uint2 x = lds64(at);
-            w[e][0] = x.x;
-            w[e][1] = x.y;
-          } else {
-            w[e][0] = lds32(at);
+          for (int g = 0; g < NG; ++g) {
+            plo[nt][g].x = fmaf(p0.x, va[g].y, fmaf(p1.x, vbp[g].y, plo[nt][g].x));
+            plo[nt][g].y = fmaf(p0.y, va[g].y, fmaf(p1.y, vbp[g].y, plo[nt][g].y));
+            pb[nt][g][0] =
+                transpose8(as_u32(__floats2half2_rn(p0.x * va[g].x, p0.y * va[g].x)));
+            pb[nt][g][1] =
+                transpose8(as_u32(__floats2half2_rn(p1.x * vbp[g].x, p1.y * vbp[g].x)));
+            mma_f16(ones[nt][g], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u,
+                    pb[nt][g][0], pb[nt][g][1], ones[nt][g][0], ones[nt][g][1], ones[nt][g][2],
+                    ones[nt][g][3]);
           }
         }
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j)
+        for (int g = 0; g < NG; ++g) {
+          // eight channels 64 g + 8 r + 0..7 of the keys t, t + 4 and t + 8, t + 12
+          uint32_t w[4];
 #pragma unroll
-          for (int hl = 0; hl < 2; ++hl) {  // four channels: D/8 lane / 4 + 8 j + 4 hl + 0..3
-            uint32_t v01[4], v23[4];
-            values4(__byte_perm(w[0][j], w[1][j], hl ? 0x7632 : 0x5410), step01, lo01, v01);
-            values4(__byte_perm(w[2][j], w[3][j], hl ? 0x7632 : 0x5410), step23, lo23, v23);
+          for (int e = 0; e < 4; ++e) w[e] = lds32(vb + (t + 4 * e) * (D / 2) + g * 32 + r * 4);
 #pragma unroll
-            for (int i2 = 0; i2 < 2; ++i2)
+          for (int hl = 0; hl < 2; ++hl) {
+            uint32_t x01 = __byte_perm(w[0], w[1], hl ? 0x7632 : 0x5410);
+            uint32_t x23 = __byte_perm(w[2], w[3], hl ? 0x7632 : 0x5410);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16(o[nt][4 * j + 2 * hl + i2], v01[2 * i2], v01[2 * i2 + 1], v23[2 * i2],
-                        v23[2 * i2 + 1], pb[nt][0], pb[nt][1]);
+            for (int i2 = 0; i2 < 2; ++i2) {
+              if (i2) x01 >>= 8, x23 >>= 8;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float (&x)[4] = o[nt][4 * g + 2 * hl + i2];
+                mma_f16(x, even_codes(x01), odd_codes(x01), even_codes(x23), odd_codes(x23),
+                        pb[nt][g][0], pb[nt][g][1], x[0], x[1], x[2], x[3]);
+              }
+            }
           }
+        }
       }
+      if (i % kFlush == kFlush - 1) flush();
       __syncwarp();  // every lane has read the stage
-      if (next < i1) issue(next++);
+      if (next < i1) issue(s, next++);
     }
 
+    // ---- biases off, sum(p lo) in: a group's channels all get the same
+    flush();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        float2 x = plo[nt][g];
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1)
+          x = fadd2(x, make_float2(__shfl_xor_sync(0xffffffffu, x.x, w),
+                                   __shfl_xor_sync(0xffffffffu, x.y, w)));
+#pragma unroll
+        for (int i2 = 0; i2 < 4; ++i2)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][4 * g + i2][e] += e % 2 ? x.y : x.x;
+      }
     // ---- the four warps' partial softmaxes joined, in the accumulators' own layout
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float x = l[nt][e];
+        float x = e ? l[nt].y : l[nt].x;
         x += __shfl_xor_sync(0xffffffffu, x, 4);
         x += __shfl_xor_sync(0xffffffffu, x, 8);
         x += __shfl_xor_sync(0xffffffffu, x, 16);
         if (r == 0) {
-          ml_s[(warp * TILE + 8 * nt + 2 * t + e) * 2] = m[nt][e];
+          ml_s[(warp * TILE + 8 * nt + 2 * t + e) * 2] = m2[nt][e];
           ml_s[(warp * TILE + 8 * nt + 2 * t + e) * 2 + 1] = x;
         }
       }
@@ -449,10 +531,13 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
         mg[(warp * NT * MT + nt * MT + i2) * 32 + lane] =
             make_float4(o[nt][i2][0], o[nt][i2][1], o[nt][i2][2], o[nt][i2][3]);
     __syncthreads();
+    // the ring is empty and the next segment known: its first copies fly while this one's
+    // results are joined
+    if (walk.more[(sg + 1) % 2]) begin(walk.seg[(sg + 1) % 2]);
     const bool whole = s.first && s.last;
     const long long slot = 2ll * blockIdx.x + (s.first ? 1 : 0);
-    // warp w joins the M tiles w MT / 4 ..: lane (r, t) holds channels D/8 r + 2 i, + 1 of
-    // query rows 2 t, 2 t + 1
+    // warp w joins the M tiles w MT / 4 ..: tile i holds the lane's channels 64 (i / 4) + 8 r +
+    // 2 (i % 4), + 1 of query rows 2 t, 2 t + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float f[kWarps][2], mt[2], lt[2];
@@ -486,14 +571,15 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
         x[1][2 * i2] = sum.y;
         x[1][2 * i2 + 1] = sum.w;
       }
-      const int ch = r * (D / 8) + warp * (MT / 2);
+      const int i0m = warp * (MT / 4), ch = 64 * (i0m / 4) + 8 * r + 2 * (i0m % 4);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int n = 8 * nt + 2 * t + e;
         if (n >= rows) continue;
         if (whole) {
-          const long long row = row0 + n;
-          const long long at = (s.w.q0 + row / G) * c.Hq + (long long)s.h * G + row % G;
+          const int token = (row0 + n) / G;
+          const long long at =
+              (long long)(s.w.q0 + token) * c.Hq + s.h * G + (row0 + n) - token * G;
           const float inv = lt[e] > 0.f ? 1.f / lt[e] : 0.f;
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + at * D + ch;
 #pragma unroll
@@ -514,10 +600,10 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
         }
       }
     }
-    if (s.followers) followers = s.followers, fb = s.b, fh = s.h, ft = s.tile;
+    if (threadIdx.x == 0 && s.followers) split = PartDesc{s.followers, s.b, s.h, s.tile};
     __syncthreads();
   }
-  if (threadIdx.x == 0) a.desc[blockIdx.x] = PartDesc{followers, fb, fh, ft};
+  if (threadIdx.x == 0) a.desc[blockIdx.x] = split;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // copies of a share that was never consumed (after an expired wait) must land before the
   // block's shared memory goes away
@@ -531,8 +617,15 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
 template <int D, int NT>
 cudaError_t launch(const AttnArgs& a, int* blocks, cudaStream_t s) {
   using C = RowsCfg<D, NT>;
-  const cudaError_t e = cudaFuncSetAttribute(
-      cache_attn_rows_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  // once per device: a decode step is short against the call
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && !(dev < 64 && done.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(cache_attn_rows_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::SMEM);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev);
+  }
   if (e != cudaSuccess) return e;
   *blocks = kSms * C::CTAS;  // one wave
   cache_attn_rows_kernel<D, NT><<<*blocks, kThreads, C::SMEM, s>>>(a);

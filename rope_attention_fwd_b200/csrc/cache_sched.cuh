@@ -4,6 +4,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <new>
+
 #include "cache.cuh"
 #include "serving.h"
 
@@ -32,7 +34,7 @@ __device__ __forceinline__ SeqWork load_work(const AttnArgs& a, int b) {
                   a.max_rows);
 }
 struct WorkOf {  // the lengths in device memory, as Walk reads them
-  const AttnArgs& a;
+  const AttnArgs& a;  // a kernel's __grid_constant__ parameter
   __device__ SeqWork operator()(int b) const { return load_work(a, b); }
 };
 
@@ -100,5 +102,19 @@ __device__ inline Run find_run(const AttnArgs& a, long long* scratch, int kid) {
   r.base = scratch[warps + 1];
   return r;
 }
+
+// A block's walk kept in shared memory and advanced by one thread, so that its state takes no
+// registers of the others: seg[k % 2] is the block's k-th segment.
+struct SharedWalk {
+  Walk<WorkOf> walk;
+  Segment seg[2];
+  int more[2];
+
+  __device__ void start(const AttnArgs& a, const Run& r) {
+    new (&walk) Walk<WorkOf>(WorkOf{a}, r, a.c.B);
+    advance(0);
+  }
+  __device__ void advance(int k) { more[k % 2] = walk.next(seg[k % 2]); }
+};
 
 }  // namespace ra
