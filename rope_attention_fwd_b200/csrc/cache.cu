@@ -11,6 +11,7 @@
 #include <cuda_fp16.h>
 
 #include <cmath>
+#include <cstring>
 
 #include "cache.cuh"
 #include "common.h"
@@ -51,30 +52,38 @@ struct ReadArgs {
   uint32_t* err;
 };
 
+// Eight elements of a row as they lie in memory, loaded ahead of their use.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool vec, float (&f)[8]) {
-  if (vec) {
-    if constexpr (sizeof(T) == 2) {
-      Vec<T, 8> v;
-      v.load(p);
-      v.get(f);
-    } else {
-      const float4 a = reinterpret_cast<const float4*>(p)[0];
-      const float4 b = reinterpret_cast<const float4*>(p)[1];
-      f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-      f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    }
-  } else {
+struct Raw8 {
+  static constexpr int N = sizeof(T) / 2;
+  uint4 w[N];
+  __device__ __forceinline__ void load(const T* p, bool vec) {
+    if (vec) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      Vec<T, 1> v;
-      float g[1];
-      v.load(p + j);
-      v.get(g);
-      f[j] = g[0];
+      for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+    } else {
+      T x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = p[j];
+      memcpy(w, x, sizeof(w));
     }
   }
-}
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 2) {
+          f[2 * j] = __uint_as_float(u[j] << 16);
+          f[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+        } else {
+          f[4 * i + j] = __uint_as_float(u[j]);
+        }
+      }
+    }
+  }
+};
 template <typename T>
 __device__ __forceinline__ void store8(T* p, bool vec, const float (&f)[8]) {
   if (vec) {
@@ -150,42 +159,67 @@ __device__ __forceinline__ void check_batch(const CacheDims& c, const int* indpt
   }
 }
 
-// Eight channels of a group of 64 (eight neighbouring lanes) to codes, and the group's pair.
-// The roundings are those of the documented definition, one by one.
-__device__ __forceinline__ uint32_t quantise8(float (&x)[8], bool& beyond, __half2& pair) {
-  float lo = INFINITY, hi = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (!(fabsf(x[j]) <= RA_CACHE_LIMIT)) {
-      beyond = true;
-      x[j] = isnan(x[j]) ? 0.f : copysignf(RA_CACHE_LIMIT, x[j]);
-    }
-    lo = fminf(lo, x[j]);
-    hi = fmaxf(hi, x[j]);
-  }
+// Smallest and largest of a group of 64 channels (eight neighbouring lanes); the largest is NaN
+// if any of them is.
+__device__ __forceinline__ void group_range(const float (&x)[8], float& lo, float& hi) {
+  auto min3 = [](float a, float b, float c) {
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+  };
+  auto max3 = [](float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+  };
+  lo = min3(min3(x[0], x[1], x[2]), min3(x[3], x[4], x[5]), fminf(x[6], x[7]));
+  hi = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), max3(x[6], x[7], x[7]));
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    const float y = __shfl_xor_sync(0xffffffffu, hi, o);
+    hi = max3(hi, y, y);
+  }
+}
+
+// Eight channels of a group of 64 to codes, and the group's pair.  The roundings are those of
+// the documented definition, one by one.  The whole warp takes part.
+__device__ __forceinline__ uint32_t quantise8(float (&x)[8], bool& beyond, __half2& pair) {
+  float lo, hi;
+  group_range(x, lo, hi);
+  const bool out = !(lo >= -RA_CACHE_LIMIT && hi <= RA_CACHE_LIMIT);
+  if (__any_sync(0xffffffffu, out)) {
+    beyond = beyond || out;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      x[j] = isnan(x[j]) ? 0.f : fminf(fmaxf(x[j], -RA_CACHE_LIMIT), RA_CACHE_LIMIT);
+    group_range(x, lo, hi);
   }
   const __half lo16 = __float2half_rn(lo);
   const float base = __half2float(lo16);
   const __half step16 = __float2half_rn(fmaxf(__fmul_rn(__fsub_rn(hi, base), 1.f / 15.f), 0.f));
   const float step = __half2float(step16);
   const float inv = step > 0.f ? __fdiv_rn(1.f, step) : 0.f;
+  // adding 2^23 rounds to a whole number (ties to even), which then sits in the low bits; the
+  // sum of the shifted words is the codes' word plus a constant
   uint32_t w = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float code = rintf(__fmul_rn(__fsub_rn(x[j], base), inv));
-    w |= (uint32_t)fminf(fmaxf(code, 0.f), 15.f) << (4 * j);
+    const float code = fminf(fmaxf(__fmul_rn(__fsub_rn(x[j], base), inv), 0.f), 15.f);
+    w += __float_as_uint(__fadd_rn(code, 8388608.f)) << (4 * j);
   }
+  constexpr uint32_t kBias = 0x4b000000u;
   pair = __halves2half2(step16, lo16);
-  return w;
+  return w - (kBias + (kBias << 4));  // the others' bits are shifted out
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs a) {
-  constexpr int U = D / 8;  // threads of a token
+// V: 16-byte accesses fit everywhere (and, in the half layout, partner channels are whole
+// vectors).
+template <typename T, int D, bool V>
+__global__ void __launch_bounds__(kThreads)
+    cache_append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int U = D / 8;   // threads of a token
+  constexpr int N = V ? 4 : 1;  // rows in flight
   const CacheDims& c = a.c;
   check_batch(c, a.indptr, a.kv_len, a.err, K_CACHE_APPEND);
   const int u = threadIdx.x % U, c0 = u * 8;
@@ -197,6 +231,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
       live ? page_of(c, a.table, seq, pos / kBlock, a.err, K_CACHE_APPEND) : -1;
   const int blk = live ? (pos / kBlock) % c.page_blocks : 0, row = live ? pos % kBlock : 0;
   const int h_lo = blockIdx.y * a.heads_per_chunk, h_hi = h_lo + a.heads_per_chunk;
+  const int half_r = a.r / 2;
 
   // angles of the channel pairs (interleaved) or channels (half) that lie in the rotated part
   float2 cs[8];
@@ -206,39 +241,42 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
     for (int j = 0; j < 8; ++j) {
       if (!a.half && j >= 4) continue;
       const int ch = a.half ? c0 + j : c0 + 2 * j;
-      const int m = a.half ? (ch < a.r / 2 ? ch : ch - a.r / 2) : ch / 2;
+      const int m = a.half ? (ch < half_r ? ch : ch - half_r) : ch / 2;
       if (ch < a.r) cs[j] = cos_sin((double)pos, a.freqs[m], a.amplitude);
     }
   }
-  // x (own channels of a row at p) rotated in place
-  auto rotate = [&](const T* p, bool vec, float (&x)[8]) {
-    if (c0 >= a.r) return;
-    if (a.half) {
-      float y[8];  // the partner channels
-      const int first = c0 < a.r / 2 ? c0 + a.r / 2 : c0 - a.r / 2;
-      if ((a.r / 2) % 8 == 0) {
-        load8(p + first, vec, y);
+  // rotated rows: own channels and, in the half layout, the partners
+  struct Pair {
+    Raw8<T> own, other;
+  };
+  auto load = [&](const RowPtr& p, int h, bool rotated, Pair& x) {
+    const T* src = static_cast<const T*>(p.in) + (int64_t)t * p.in_n + (int64_t)h * p.in_h;
+    x.own.load(src + c0, V);
+    if (rotated && a.half && c0 < a.r) {
+      if constexpr (V) {
+        x.other.load(src + (c0 < half_r ? c0 + half_r : c0 - half_r), true);
       } else {
+        T y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int ch = c0 + j;
-          y[j] = 0.f;
-          if (ch < a.r) {
-            Vec<T, 1> v;
-            float g[1];
-            v.load(p + (ch < a.r / 2 ? ch + a.r / 2 : ch - a.r / 2));
-            v.get(g);
-            y[j] = g[0];
-          }
+          const int ch = c0 + j;  // not rotated: itself, unused
+          y[j] = src[ch >= a.r ? ch : ch < half_r ? ch + half_r : ch - half_r];
         }
+        memcpy(x.other.w, y, sizeof(y));
       }
+    }
+  };
+  auto rotate = [&](const Pair& p, float (&x)[8]) {
+    p.own.get(x);
+    if (c0 >= a.r) return;
+    if (a.half) {
+      float y[8];
+      p.other.get(y);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int ch = c0 + j;
-        if (ch < a.r / 2)
-          x[j] = turn(cs[j], x[j], y[j]).x;
-        else if (ch < a.r)
-          x[j] = turn(cs[j], y[j], x[j]).y;
+        if (ch < half_r) x[j] = turn(cs[j], x[j], y[j]).x;
+        else if (ch < a.r) x[j] = turn(cs[j], y[j], x[j]).y;
       }
     } else {
 #pragma unroll
@@ -252,51 +290,71 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
   };
 
   bool beyond = false;
-  for (int h = h_lo; h < h_hi && h < 2 * c.Hkv + (a.q.in ? c.Hq : 0); ++h) {
-    if (h < 2 * c.Hkv) {
-      // keys (rotated), then values: the whole warp takes part in the groups' shuffles
-      const bool is_k = h < c.Hkv;
-      const int hh = is_k ? h : h - c.Hkv;
-      const RowPtr& p = is_k ? a.k : a.v;
-      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  // keys (rotated), then values: the whole warp takes part in the groups' shuffles
+#pragma unroll
+  for (int z = 0; z < 2; ++z) {
+    const RowPtr& p = z == 0 ? a.k : a.v;
+    const int first = max(0, h_lo - z * c.Hkv), last = min(c.Hkv, h_hi - z * c.Hkv);
+    for (int h = first; h < last; h += N) {
+      Pair raw[N];
       if (live) {
-        const T* src = static_cast<const T*>(p.in) + (int64_t)t * p.in_n + (int64_t)hh * p.in_h;
-        load8(src + c0, p.vec, x);
-        if (is_k) rotate(src, p.vec, x);
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (h + e < last) load(p, h + e, z == 0, raw[e]);
       }
-      __half2 pair;
-      const uint32_t w = quantise8(x, beyond, pair);
-      if (page >= 0) {
-        uint8_t* block =
-            a.cache + block_at(c, page, hh, blk) + (is_k ? 0 : value_offset(D));
-        *reinterpret_cast<uint32_t*>(block + row * (D / 2) + u * 4) = w;
-        if (u % 8 == 0)
-          *reinterpret_cast<__half2*>(block + code_bytes(D) + (row * (D / kGroup) + u / 8) * 4) =
-              pair;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        if (h + e >= last) break;
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (live) {
+          if (z == 0) rotate(raw[e], x);
+          else raw[e].own.get(x);
+        }
+        __half2 pair;
+        const uint32_t w = quantise8(x, beyond, pair);
+        if (page >= 0) {
+          uint8_t* block = a.cache + block_at(c, page, h + e, blk) + (z == 0 ? 0 : value_offset(D));
+          *reinterpret_cast<uint32_t*>(block + row * (D / 2) + u * 4) = w;
+          if (u % 8 == 0)
+            *reinterpret_cast<__half2*>(block + code_bytes(D) +
+                                        (row * (D / kGroup) + u / 8) * 4) = pair;
+        }
       }
-    } else {
-      const int hh = h - 2 * c.Hkv;
-      float x[8];
+    }
+  }
+  if (a.q.in) {
+    const int first = max(0, h_lo - 2 * c.Hkv), last = min(c.Hq, h_hi - 2 * c.Hkv);
+    for (int h = first; h < last; h += N) {
+      Pair raw[N];
       if (live) {
-        const T* src = static_cast<const T*>(a.q.in) + (int64_t)t * a.q.in_n +
-                       (int64_t)hh * a.q.in_h;
-        load8(src + c0, a.q.vec, x);
-        rotate(src, a.q.vec, x);
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (h + e < last) load(a.q, h + e, true, raw[e]);
       }
       // in place, a half-layout row's partner channels are read by other lanes of the warp
       // before any lane writes its own
       __syncwarp();
-      if (live)
-        store8(static_cast<T*>(a.q.out) + (int64_t)t * a.q.out_n + (int64_t)hh * a.q.out_h + c0,
-               a.q.vec, x);
+      if (live) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          if (h + e >= last) break;
+          float x[8];
+          rotate(raw[e], x);
+          store8(static_cast<T*>(a.q.out) + (int64_t)t * a.q.out_n +
+                     (int64_t)(h + e) * a.q.out_h + c0,
+                 V, x);
+        }
+      }
     }
   }
   if (beyond) atomicCAS(a.err, 0u, (uint32_t)RA_ERR_RANGE);
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kThreads)
+    cache_read_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int U = D / 8;
+  constexpr int N = 8;  // rows in flight
   const CacheDims& c = a.c;
   check_batch(c, a.indptr, a.kv_len, a.err, K_CACHE_READ);
   const int u = threadIdx.x % U, c0 = u * 8;
@@ -306,25 +364,43 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a) 
   if (pos < 0) return;
   const int page = page_of(c, a.table, seq, pos / kBlock, a.err, K_CACHE_READ);
   const int blk = (pos / kBlock) % c.page_blocks, row = pos % kBlock;
-  const int h_lo = blockIdx.y * a.heads_per_chunk;
-  const int h_hi = min(h_lo + a.heads_per_chunk, 2 * c.Hkv);
-#pragma unroll 4
-  for (int h = h_lo; h < h_hi; ++h) {
-    const bool is_k = h < c.Hkv;
-    const int hh = is_k ? h : h - c.Hkv;
-    const RowPtr& p = is_k ? a.k : a.v;
-    if (!p.out) continue;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (page >= 0) {
-      const uint8_t* block = a.cache + block_at(c, page, hh, blk) + (is_k ? 0 : value_offset(D));
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(block + row * (D / 2) + u * 4);
-      const float2 pair = __half22float2(*reinterpret_cast<const __half2*>(
-          block + code_bytes(D) + (row * (D / kGroup) + u / 8) * 4));
+  const int h_lo = blockIdx.y * a.heads_per_chunk, h_hi = h_lo + a.heads_per_chunk;
+  // a head's block is the same distance after the one before it
+  const size_t head_bytes = (size_t)c.page_blocks * block_bytes(D);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)  // step * code is exact in fp32: one rounding, of the sum
-        x[j] = fmaf(pair.x, (float)((w >> (4 * j)) & 15u), pair.y);
+  for (int z = 0; z < 2; ++z) {
+    const RowPtr& p = z == 0 ? a.k : a.v;
+    if (!p.out) continue;
+    const int first = max(0, h_lo - z * c.Hkv), last = min(c.Hkv, h_hi - z * c.Hkv);
+    if (first >= last) continue;
+    const uint8_t* src = a.cache + (page >= 0 ? block_at(c, page, first, blk) : 0) +
+                         (z == 0 ? 0 : value_offset(D));
+    const uint8_t* codes = src + row * (D / 2) + u * 4;
+    const uint8_t* pairs = src + code_bytes(D) + (row * (D / kGroup) + u / 8) * 4;
+    T* dst = static_cast<T*>(p.out) + (int64_t)t * p.out_n + (int64_t)first * p.out_h + c0;
+    for (int h = first; h < last; h += N) {
+      uint32_t w[N], pr[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        w[e] = pr[e] = 0u;  // a bad page: zeros
+        if (page >= 0 && h + e < last) {
+          w[e] = *reinterpret_cast<const uint32_t*>(codes + (size_t)(h - first + e) * head_bytes);
+          pr[e] = *reinterpret_cast<const uint32_t*>(pairs + (size_t)(h - first + e) * head_bytes);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        if (h + e >= last) break;
+        const float2 pair = __half22float2(*reinterpret_cast<const __half2*>(&pr[e]));
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)  // step * code is exact in fp32: one rounding, of the sum
+          x[j] = fmaf(pair.x,
+                      __uint_as_float(((w[e] >> (4 * j)) & 15u) | 0x4b000000u) - 8388608.f,
+                      pair.y);
+        store8(dst + (int64_t)(h - first + e) * p.out_h, p.vec, x);
+      }
     }
-    store8(static_cast<T*>(p.out) + (int64_t)t * p.out_n + (int64_t)hh * p.out_h + c0, p.vec, x);
   }
 }
 
@@ -353,6 +429,12 @@ ra_status check_token_rows(const ra_rows* r, const ra_cache& p, int64_t H, bool 
 int vectors_fit(const ra_rows& r, int32_t dtype) {
   const int64_t V = (int64_t)(16 / elem_bytes(dtype));
   return aligned_to(r.ptr, 16) && r.stride_n % V == 0 && r.stride_h % V == 0;
+}
+
+template <typename T, int D>
+void launch_append(const AppendArgs& a, dim3 grid, bool vec, cudaStream_t s) {
+  if (vec) cache_append_kernel<T, D, true><<<grid, kThreads, 0, s>>>(a);
+  else cache_append_kernel<T, D, false><<<grid, kThreads, 0, s>>>(a);
 }
 
 // Heads per block: all of them, or fewer until the launch has about eight blocks per SM.
@@ -463,12 +545,13 @@ ra_status rope_attn_cache_append(const ra_cache* p, void* cache, const int32_t* 
   const dim3 grid((unsigned)gx, (unsigned)((heads + a.heads_per_chunk - 1) / a.heads_per_chunk));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const TimingScope timed(K_CACHE_APPEND, s);
+  const bool vec = a.k.vec && a.v.vec && (!q || a.q.vec) && (!a.half || (a.r / 2) % 8 == 0);
   if (p->dtype == RA_BF16) {
-    if (p->d == 64) cache_append_kernel<__nv_bfloat16, 64><<<grid, kThreads, 0, s>>>(a);
-    else cache_append_kernel<__nv_bfloat16, 128><<<grid, kThreads, 0, s>>>(a);
+    if (p->d == 64) launch_append<__nv_bfloat16, 64>(a, grid, vec, s);
+    else launch_append<__nv_bfloat16, 128>(a, grid, vec, s);
   } else {
-    if (p->d == 64) cache_append_kernel<float, 64><<<grid, kThreads, 0, s>>>(a);
-    else cache_append_kernel<float, 128><<<grid, kThreads, 0, s>>>(a);
+    if (p->d == 64) launch_append<float, 64>(a, grid, vec, s);
+    else launch_append<float, 128>(a, grid, vec, s);
   }
   return cudaGetLastError() == cudaSuccess ? RA_OK : RA_ERR_CUDA;
 }
