@@ -199,7 +199,7 @@ __device__ __forceinline__ uint32_t quantise8(float (&x)[8], bool& beyond, __hal
   const float base = __half2float(lo16);
   const __half step16 = __float2half_rn(fmaxf(__fmul_rn(__fsub_rn(hi, base), 1.f / 15.f), 0.f));
   const float step = __half2float(step16);
-  const float inv = step > 0.f ? __fdiv_rn(1.f, step) : 0.f;
+  const float inv = step > 0.f ? __frcp_rn(step) : 0.f;
   // adding 2^23 rounds to a whole number (ties to even), which then sits in the low bits; the
   // sum of the shifted words is the codes' word plus a constant
   uint32_t w = 0;
@@ -213,13 +213,14 @@ __device__ __forceinline__ uint32_t quantise8(float (&x)[8], bool& beyond, __hal
   return w - (kBias + (kBias << 4));  // the others' bits are shifted out
 }
 
-// V: 16-byte accesses fit everywhere (and, in the half layout, partner channels are whole
-// vectors).
-template <typename T, int D, bool V>
+// V: 16-byte accesses fit everywhere and a thread's eight channels are rotated alike: all of
+// them or none, in the half layout all of the same half (partners are then whole vectors).
+template <typename T, int D, bool V, bool HALF>
 __global__ void __launch_bounds__(kThreads)
     cache_append_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int U = D / 8;   // threads of a token
+  constexpr int U = D / 8;      // threads of a token
   constexpr int N = V ? 4 : 1;  // rows in flight
+  constexpr int NP = HALF ? 8 : 4;
   const CacheDims& c = a.c;
   check_batch(c, a.indptr, a.kv_len, a.err, K_CACHE_APPEND);
   const int u = threadIdx.x % U, c0 = u * 8;
@@ -229,20 +230,20 @@ __global__ void __launch_bounds__(kThreads)
   const bool live = pos >= 0;
   const int page =
       live ? page_of(c, a.table, seq, pos / kBlock, a.err, K_CACHE_APPEND) : -1;
-  const int blk = live ? (pos / kBlock) % c.page_blocks : 0, row = live ? pos % kBlock : 0;
   const int h_lo = blockIdx.y * a.heads_per_chunk, h_hi = h_lo + a.heads_per_chunk;
   const int half_r = a.r / 2;
+  const bool turned = c0 < a.r;  // V: all eight channels
 
-  // angles of the channel pairs (interleaved) or channels (half) that lie in the rotated part
-  float2 cs[8];
-  const bool turns = live && (h_lo < c.Hkv || h_hi > 2 * c.Hkv) && c0 < a.r;
-  if (turns) {
+  // (cos, sin) of the channel pairs, or per channel with the sine's sign as the partner enters
+  // (first half: x cos - partner sin; second: x cos + partner sin); not rotated: unused
+  float2 cs[NP];
+  if (live && turned && (h_lo < c.Hkv || h_hi > 2 * c.Hkv)) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (!a.half && j >= 4) continue;
-      const int ch = a.half ? c0 + j : c0 + 2 * j;
-      const int m = a.half ? (ch < half_r ? ch : ch - half_r) : ch / 2;
-      if (ch < a.r) cs[j] = cos_sin((double)pos, a.freqs[m], a.amplitude);
+    for (int j = 0; j < NP; ++j) {
+      const int ch = HALF ? c0 + j : c0 + 2 * j;
+      const int m = HALF ? (ch < half_r ? ch : ch - half_r) : ch / 2;
+      if (V || ch < a.r) cs[j] = cos_sin((double)pos, a.freqs[m], a.amplitude);
+      if (HALF && ch < half_r) cs[j].y = -cs[j].y;
     }
   }
   // rotated rows: own channels and, in the half layout, the partners
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kThreads)
   auto load = [&](const RowPtr& p, int h, bool rotated, Pair& x) {
     const T* src = static_cast<const T*>(p.in) + (int64_t)t * p.in_n + (int64_t)h * p.in_h;
     x.own.load(src + c0, V);
-    if (rotated && a.half && c0 < a.r) {
+    if (HALF && rotated && turned) {
       if constexpr (V) {
         x.other.load(src + (c0 < half_r ? c0 + half_r : c0 - half_r), true);
       } else {
@@ -268,33 +269,41 @@ __global__ void __launch_bounds__(kThreads)
   };
   auto rotate = [&](const Pair& p, float (&x)[8]) {
     p.own.get(x);
-    if (c0 >= a.r) return;
-    if (a.half) {
+    if (!turned) return;
+    if constexpr (HALF) {
       float y[8];
       p.other.get(y);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int ch = c0 + j;
-        if (ch < half_r) x[j] = turn(cs[j], x[j], y[j]).x;
-        else if (ch < a.r) x[j] = turn(cs[j], y[j], x[j]).y;
-      }
+      for (int j = 0; j < 8; ++j)
+        if (V || c0 + j < a.r)
+          x[j] = __fadd_rn(__fmul_rn(cs[j].x, x[j]), __fmul_rn(cs[j].y, y[j]));
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (c0 + 2 * j >= a.r) break;
-        const float2 y = turn(cs[j], x[2 * j], x[2 * j + 1]);
-        x[2 * j] = y.x;
-        x[2 * j + 1] = y.y;
-      }
+      for (int j = 0; j < 4; ++j)
+        if (V || c0 + 2 * j < a.r) {
+          const float2 y = turn(cs[j], x[2 * j], x[2 * j + 1]);
+          x[2 * j] = y.x;
+          x[2 * j + 1] = y.y;
+        }
     }
   };
 
   bool beyond = false;
   // keys (rotated), then values: the whole warp takes part in the groups' shuffles
+  const size_t head_bytes = (size_t)c.page_blocks * block_bytes(D);
 #pragma unroll
   for (int z = 0; z < 2; ++z) {
     const RowPtr& p = z == 0 ? a.k : a.v;
     const int first = max(0, h_lo - z * c.Hkv), last = min(c.Hkv, h_hi - z * c.Hkv);
+    if (first >= last) continue;
+    uint8_t* codes = nullptr;  // of head `first`
+    uint8_t* pairs = nullptr;
+    if (page >= 0) {
+      uint8_t* block = a.cache + block_at(c, page, first, (pos / kBlock) % c.page_blocks) +
+                       (z == 0 ? 0 : value_offset(D));
+      codes = block + pos % kBlock * (D / 2) + u * 4;
+      pairs = block + code_bytes(D) + (pos % kBlock * (D / kGroup) + u / 8) * 4;
+    }
     for (int h = first; h < last; h += N) {
       Pair raw[N];
       if (live) {
@@ -313,11 +322,9 @@ __global__ void __launch_bounds__(kThreads)
         __half2 pair;
         const uint32_t w = quantise8(x, beyond, pair);
         if (page >= 0) {
-          uint8_t* block = a.cache + block_at(c, page, h + e, blk) + (z == 0 ? 0 : value_offset(D));
-          *reinterpret_cast<uint32_t*>(block + row * (D / 2) + u * 4) = w;
+          *reinterpret_cast<uint32_t*>(codes + (size_t)(h - first + e) * head_bytes) = w;
           if (u % 8 == 0)
-            *reinterpret_cast<__half2*>(block + code_bytes(D) +
-                                        (row * (D / kGroup) + u / 8) * 4) = pair;
+            *reinterpret_cast<__half2*>(pairs + (size_t)(h - first + e) * head_bytes) = pair;
         }
       }
     }
@@ -433,8 +440,10 @@ int vectors_fit(const ra_rows& r, int32_t dtype) {
 
 template <typename T, int D>
 void launch_append(const AppendArgs& a, dim3 grid, bool vec, cudaStream_t s) {
-  if (vec) cache_append_kernel<T, D, true><<<grid, kThreads, 0, s>>>(a);
-  else cache_append_kernel<T, D, false><<<grid, kThreads, 0, s>>>(a);
+  if (vec && a.half) cache_append_kernel<T, D, true, true><<<grid, kThreads, 0, s>>>(a);
+  else if (vec) cache_append_kernel<T, D, true, false><<<grid, kThreads, 0, s>>>(a);
+  else if (a.half) cache_append_kernel<T, D, false, true><<<grid, kThreads, 0, s>>>(a);
+  else cache_append_kernel<T, D, false, false><<<grid, kThreads, 0, s>>>(a);
 }
 
 // Heads per block: all of them, or fewer until the launch has about eight blocks per SM.
@@ -545,7 +554,7 @@ ra_status rope_attn_cache_append(const ra_cache* p, void* cache, const int32_t* 
   const dim3 grid((unsigned)gx, (unsigned)((heads + a.heads_per_chunk - 1) / a.heads_per_chunk));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const TimingScope timed(K_CACHE_APPEND, s);
-  const bool vec = a.k.vec && a.v.vec && (!q || a.q.vec) && (!a.half || (a.r / 2) % 8 == 0);
+  const bool vec = a.k.vec && a.v.vec && (!q || a.q.vec) && a.r % (a.half ? 16 : 8) == 0;
   if (p->dtype == RA_BF16) {
     if (p->d == 64) launch_append<__nv_bfloat16, 64>(a, grid, vec, s);
     else launch_append<__nv_bfloat16, 128>(a, grid, vec, s);
