@@ -216,12 +216,14 @@ __device__ __forceinline__ uint32_t quantise8(float (&x)[8], bool& beyond, __hal
 // V: 16-byte accesses fit everywhere and a thread's eight channels are rotated alike: all of
 // them or none, in the half layout all of the same half (partners are then whole vectors).
 template <typename T, int D, bool V, bool HALF>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 6)
     cache_append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int U = D / 8;      // threads of a token
   constexpr int N = V ? 4 : 1;  // rows in flight
   constexpr int NP = HALF ? 8 : 4;
   const CacheDims& c = a.c;
+  grid_wait();
+  grid_release();
   check_batch(c, a.indptr, a.kv_len, a.err, K_CACHE_APPEND);
   const int u = threadIdx.x % U, c0 = u * 8;
   const int t = blockIdx.x * (kThreads / U) + threadIdx.x / U;
@@ -363,6 +365,8 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int U = D / 8;
   constexpr int N = 8;  // rows in flight
   const CacheDims& c = a.c;
+  grid_wait();
+  grid_release();
   check_batch(c, a.indptr, a.kv_len, a.err, K_CACHE_READ);
   const int u = threadIdx.x % U, c0 = u * 8;
   const int t = blockIdx.x * (kThreads / U) + threadIdx.x / U;
@@ -439,11 +443,13 @@ int vectors_fit(const ra_rows& r, int32_t dtype) {
 }
 
 template <typename T, int D>
-void launch_append(const AppendArgs& a, dim3 grid, bool vec, cudaStream_t s) {
-  if (vec && a.half) cache_append_kernel<T, D, true, true><<<grid, kThreads, 0, s>>>(a);
-  else if (vec) cache_append_kernel<T, D, true, false><<<grid, kThreads, 0, s>>>(a);
-  else if (a.half) cache_append_kernel<T, D, false, true><<<grid, kThreads, 0, s>>>(a);
-  else cache_append_kernel<T, D, false, false><<<grid, kThreads, 0, s>>>(a);
+cudaError_t launch_append(const AppendArgs& a, dim3 grid, bool vec, cudaStream_t s) {
+  if (vec && a.half)
+    return launch_overlapped(cache_append_kernel<T, D, true, true>, grid, kThreads, 0, s, a);
+  if (vec) return launch_overlapped(cache_append_kernel<T, D, true, false>, grid, kThreads, 0, s, a);
+  if (a.half)
+    return launch_overlapped(cache_append_kernel<T, D, false, true>, grid, kThreads, 0, s, a);
+  return launch_overlapped(cache_append_kernel<T, D, false, false>, grid, kThreads, 0, s, a);
 }
 
 // Heads per block: all of them, or fewer until the launch has about eight blocks per SM.
@@ -555,14 +561,14 @@ ra_status rope_attn_cache_append(const ra_cache* p, void* cache, const int32_t* 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const TimingScope timed(K_CACHE_APPEND, s);
   const bool vec = a.k.vec && a.v.vec && (!q || a.q.vec) && a.r % (a.half ? 16 : 8) == 0;
-  if (p->dtype == RA_BF16) {
-    if (p->d == 64) launch_append<__nv_bfloat16, 64>(a, grid, vec, s);
-    else launch_append<__nv_bfloat16, 128>(a, grid, vec, s);
-  } else {
-    if (p->d == 64) launch_append<float, 64>(a, grid, vec, s);
-    else launch_append<float, 128>(a, grid, vec, s);
-  }
-  return cudaGetLastError() == cudaSuccess ? RA_OK : RA_ERR_CUDA;
+  cudaError_t e;
+  if (p->dtype == RA_BF16)
+    e = p->d == 64 ? launch_append<__nv_bfloat16, 64>(a, grid, vec, s)
+                   : launch_append<__nv_bfloat16, 128>(a, grid, vec, s);
+  else
+    e = p->d == 64 ? launch_append<float, 64>(a, grid, vec, s)
+                   : launch_append<float, 128>(a, grid, vec, s);
+  return e == cudaSuccess ? RA_OK : RA_ERR_CUDA;
 }
 
 ra_status rope_attn_cache_read(const ra_cache* p, const void* cache, const int32_t* table,
@@ -588,14 +594,12 @@ ra_status rope_attn_cache_read(const ra_cache* p, const void* cache, const int32
                   (unsigned)((2 * p->Hkv + a.heads_per_chunk - 1) / a.heads_per_chunk));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const TimingScope timed(K_CACHE_READ, s);
-  if (p->dtype == RA_BF16) {
-    if (p->d == 64) cache_read_kernel<__nv_bfloat16, 64><<<grid, kThreads, 0, s>>>(a);
-    else cache_read_kernel<__nv_bfloat16, 128><<<grid, kThreads, 0, s>>>(a);
-  } else {
-    if (p->d == 64) cache_read_kernel<float, 64><<<grid, kThreads, 0, s>>>(a);
-    else cache_read_kernel<float, 128><<<grid, kThreads, 0, s>>>(a);
-  }
-  return cudaGetLastError() == cudaSuccess ? RA_OK : RA_ERR_CUDA;
+  void (*kernel)(ReadArgs) =
+      p->dtype == RA_BF16
+          ? (p->d == 64 ? cache_read_kernel<__nv_bfloat16, 64> : cache_read_kernel<__nv_bfloat16, 128>)
+          : (p->d == 64 ? cache_read_kernel<float, 64> : cache_read_kernel<float, 128>);
+  const cudaError_t e = launch_overlapped(kernel, grid, kThreads, 0, s, a);
+  return e == cudaSuccess ? RA_OK : RA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -29,7 +29,7 @@ namespace {
 constexpr int kF32Threads = 128;
 
 template <int D, int R>
-__global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int DL = D / 32;  // channels of a lane in the value product
   __shared__ __align__(16) float q_s[R][D];
   __shared__ __align__(16) float p_s[4][32][R];
@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const AttnA
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const float scale_log2 = c.scale * 1.4426950408889634f;
 
+  grid_wait();
   const Run run = find_run(a, scratch, K_CACHE_ATTN_F32);
   Walk<WorkOf> walk(WorkOf{a}, run, c.B);
   Segment s;
@@ -217,6 +218,7 @@ __global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const AttnA
     __syncthreads();
   }
   if (threadIdx.x == 0) a.desc[blockIdx.x] = PartDesc{followers, fb, fh, ft};
+  grid_release();
 }
 
 // ------------------------------------------------------------------ joining split items
@@ -237,7 +239,8 @@ __global__ void __launch_bounds__(kCombineThreads)
     cache_combine_kernel(const __grid_constant__ CombineArgs ca) {
   constexpr int DL = D / 32;
   __shared__ float red[kCombineWarps][D], red_l[kCombineWarps], mx_s[kCombineWarps];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait();
+  grid_release();
   const int which = (int)blockIdx.x < ca.blocks[0] ? 0 : 1;
   const AttnArgs& a = ca.a[which];
   const int first = blockIdx.x - (which ? ca.blocks[0] : 0);
@@ -345,45 +348,28 @@ __global__ void __launch_bounds__(kCombineThreads)
 template <int D>
 cudaError_t launch_f32(AttnArgs& a, int rows, cudaStream_t s) {
   // the smallest tile that holds the rows of the longest sequence
-  if (rows <= 1) {
-    a.tile = 1;
-    cache_attn_f32_kernel<D, 1><<<kRowsBlocks, kF32Threads, 0, s>>>(a);
-  } else if (rows <= 2) {
-    a.tile = 2;
-    cache_attn_f32_kernel<D, 2><<<kRowsBlocks, kF32Threads, 0, s>>>(a);
-  } else if (rows <= 4) {
-    a.tile = 4;
-    cache_attn_f32_kernel<D, 4><<<kRowsBlocks, kF32Threads, 0, s>>>(a);
-  } else {
-    a.tile = 8;
-    cache_attn_f32_kernel<D, 8><<<kRowsBlocks, kF32Threads, 0, s>>>(a);
-  }
-  return cudaGetLastError();
+  void (*kernel)(AttnArgs);
+  if (rows <= 1) a.tile = 1, kernel = cache_attn_f32_kernel<D, 1>;
+  else if (rows <= 2) a.tile = 2, kernel = cache_attn_f32_kernel<D, 2>;
+  else if (rows <= 4) a.tile = 4, kernel = cache_attn_f32_kernel<D, 4>;
+  else a.tile = 8, kernel = cache_attn_f32_kernel<D, 8>;
+  return launch_overlapped(kernel, dim3(kRowsBlocks), kF32Threads, 0, s, a);
 }
 
 }  // namespace
 
 namespace {
 
-// The combine launch overlaps its start with the attention kernel's end (programmatic stream
-// serialisation: it waits for that kernel's writes before it reads any).  rows: most rows of
-// an item.
+// rows: most rows of an item.
 cudaError_t launch_combine(const CombineArgs& ca, int32_t dtype, int d, int rows,
                            cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(ca.blocks[0] + ca.blocks[1]), (unsigned)std::min(rows, 32));
-  cfg.blockDim = dim3(kCombineThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (dtype == RA_BF16)
-    return d == 64 ? cudaLaunchKernelEx(&cfg, cache_combine_kernel<__nv_bfloat16, 64>, ca)
-                   : cudaLaunchKernelEx(&cfg, cache_combine_kernel<__nv_bfloat16, 128>, ca);
-  return d == 64 ? cudaLaunchKernelEx(&cfg, cache_combine_kernel<float, 64>, ca)
-                 : cudaLaunchKernelEx(&cfg, cache_combine_kernel<float, 128>, ca);
+  void (*kernel)(CombineArgs) =
+      dtype == RA_BF16
+          ? (d == 64 ? cache_combine_kernel<__nv_bfloat16, 64>
+                     : cache_combine_kernel<__nv_bfloat16, 128>)
+          : (d == 64 ? cache_combine_kernel<float, 64> : cache_combine_kernel<float, 128>);
+  const dim3 grid((unsigned)(ca.blocks[0] + ca.blocks[1]), (unsigned)std::min(rows, 32));
+  return launch_overlapped(kernel, grid, kCombineThreads, 0, s, ca);
 }
 
 }  // namespace

@@ -104,7 +104,7 @@ __device__ __forceinline__ StepRange tile_steps(const CacheDims& c, const Segmen
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __grid_constant__ AttnArgs a) {
   using C = ChunkCfg<D>;
   constexpr int KID = K_CACHE_ATTN_CHUNK;
   constexpr int NG = D / kGroup;
@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const Att
     *abort_flag = 0;
     fence_barrier_init();
   }
+  grid_wait();
   const Run run = find_run(a, scratch, KID);
   // a block without work (an idle one of a small launch) takes no TMEM and waits for nothing
   if (run.begin >= run.end) {
@@ -548,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const Att
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_release();
 }
 
 template <int D>
@@ -564,8 +565,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev);
   }
   if (e != cudaSuccess) return e;
-  cache_attn_chunk_kernel<D><<<kChunkBlocks, kThreads, C::SMEM, s>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(cache_attn_chunk_kernel<D>, dim3(kChunkBlocks), kThreads, C::SMEM, s, a);
 }
 
 }  // namespace

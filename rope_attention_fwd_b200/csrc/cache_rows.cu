@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
   }
   __syncwarp();
   SharedWalk& walk = *reinterpret_cast<SharedWalk*>(smem + C::OFF_WALK);
+  grid_wait();
   {
     const Run run =
         find_run(a, reinterpret_cast<long long*>(smem + C::OFF_SCRATCH), K_CACHE_ATTN);
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
     __syncthreads();
   }
   if (threadIdx.x == 0) a.desc[blockIdx.x] = split;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_release();
   // copies of a share that was never consumed (after an expired wait) must land before the
   // block's shared memory goes away
   int dummy = 0;
@@ -628,8 +629,7 @@ cudaError_t launch(const AttnArgs& a, int* blocks, cudaStream_t s) {
   }
   if (e != cudaSuccess) return e;
   *blocks = kSms * C::CTAS;  // one wave
-  cache_attn_rows_kernel<D, NT><<<*blocks, kThreads, C::SMEM, s>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(cache_attn_rows_kernel<D, NT>, dim3(*blocks), kThreads, C::SMEM, s, a);
 }
 
 }  // namespace

@@ -38,6 +38,34 @@ struct TimingScope {
   TimingScope& operator=(const TimingScope&) = delete;
 };
 
+// A launch that may begin while the kernel before it on the stream drains (programmatic stream
+// serialisation).  Such a kernel calls grid_wait() before it touches global memory, which
+// returns once everything before it on the stream is complete and visible, and grid_release()
+// when the next launch may be brought up beside it.
+template <typename... P, typename... A>
+inline cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem,
+                                     cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void grid_release() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+#endif
+
 struct DevCtl {
   uint32_t* err;        // workspace error word
   uint64_t wait_ns;     // bound on every device-side wait

@@ -51,7 +51,8 @@ struct RotArgs {
 // V: elements of one access (a 16-byte vector, or 1 where sizes, strides or addresses allow
 // no vector).
 template <typename T, int V, bool HALF, bool BWD>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotArgs a) {
+__global__ void __launch_bounds__(kThreads)
+    rotary_kernel(const __grid_constant__ RotArgs a) {
   constexpr int W = HALF ? V : (V > 1 ? V : 2);      // channels of the first (or only) piece
   constexpr int NP = HALF ? V : W / 2;               // pairs of a unit
   constexpr int NV = HALF || V == 1 ? 2 : 1;         // accesses of a unit
@@ -62,6 +63,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotArgs a) {
   const int c1 = HALF ? c0 + a.r / 2 : c0 + 1;       // second access (rotated units only)
   const int m0 = HALF ? c0 : c0 / 2;
   const int lo = blockIdx.y * a.heads_per_chunk, hi = lo + a.heads_per_chunk;
+  grid_wait();
+  grid_release();
   const long long tiles = (a.tokens + a.tile - 1) / a.tile;
   const bool torque = BWD && a.part != nullptr;
   double acc[NP];
@@ -171,6 +174,8 @@ __global__ void __launch_bounds__(128)
                          const double* __restrict__ freqs, float* __restrict__ dalpha) {
   __shared__ double red[128];
   const int m = blockIdx.x;
+  grid_wait();
+  grid_release();
   double s = 0.0;
   for (int k = threadIdx.x; k < parts; k += 128) s += part[(long long)k * M + m];
   red[threadIdx.x] = s;
@@ -196,6 +201,8 @@ __global__ void rotary_freqs_kernel(const ra_rotary r, const float* __restrict__
     g = fmin(1.0, fmax(0.0, g));
     t = (1.0 - g) * t / r.factor + g * t;
   }
+  grid_wait();  // the fixed part was formed beside the kernel before
+  grid_release();
   if (alpha) t *= exp((double)alpha[m]);
   freqs[m] = m >= M - r.fixed_bands ? 0.0 : t;
 }
@@ -249,8 +256,7 @@ cudaError_t launch_rot(const RotArgs& a, dim3 grid, cudaStream_t s) {
   constexpr int NP = HALF ? V : (V > 1 ? V / 2 : 1);
   const size_t smem =
       BWD && a.part ? sizeof(double) * (size_t)a.rot_units * NP * (size_t)a.tile : 0;
-  rotary_kernel<T, V, HALF, BWD><<<grid, kThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(rotary_kernel<T, V, HALF, BWD>, grid, kThreads, smem, s, a);
 }
 
 template <typename T, bool BWD>
@@ -296,14 +302,19 @@ ra_status run(const ra_rotary* r, int64_t B, int64_t n, int32_t dtype, const dou
   const long long tiles = (a.tokens + a.tile - 1) / a.tile;
   // Few tokens: the heads are split over the blocks' second dimension, at least kUnroll heads
   // each, until there are about eight blocks per SM (the angles are then formed once per
-  // chunk, which idle SMs do for nothing).
-  const long long want = (kRotaryBlocks + tiles - 1) / tiles;
+  // chunk, which idle SMs do for nothing).  With partial torques there are at most kRotaryParts
+  // blocks: chunks as far as that leaves one tile per block, else equal numbers of tiles.
+  const long long want = part ? std::max<long long>(1, kRotaryParts / tiles)
+                              : (kRotaryBlocks + tiles - 1) / tiles;
   const int64_t chunks = std::max<int64_t>(
       1, std::min<int64_t>(want, (heads + kUnroll - 1) / kUnroll));
   a.heads_per_chunk = (int)((heads + chunks - 1) / chunks);
   const unsigned gy = (unsigned)((heads + a.heads_per_chunk - 1) / a.heads_per_chunk);
   long long gx = tiles;
-  if (part) gx = std::min<long long>(gx, std::max<long long>(1, kRotaryParts / gy));
+  if (part) {
+    const long long rounds = (tiles * gy + kRotaryParts - 1) / kRotaryParts;
+    gx = (tiles + rounds - 1) / rounds;
+  }
   if (gx > 0x7fffffff) return RA_ERR_UNSUPPORTED;
   if (parts) *parts = (int)(gx * gy);
   const dim3 grid((unsigned)gx, gy);
@@ -367,8 +378,10 @@ ra_status rope_attn_rotary_freqs(const ra_rotary* r, const float* alpha, double*
   if (!freqs || !aligned_to(freqs, 8) || !aligned_to(alpha, 4)) return RA_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const TimingScope timed(K_ROTARY_FREQS, s);
-  rotary_freqs_kernel<<<(unsigned)((r->rot_dim / 2 + 31) / 32), 32, 0, s>>>(*r, alpha, freqs);
-  return cudaGetLastError() == cudaSuccess ? RA_OK : RA_ERR_CUDA;
+  const cudaError_t e = launch_overlapped(
+      rotary_freqs_kernel, dim3((unsigned)((r->rot_dim / 2 + 31) / 32)), 32, 0, s, *r, alpha,
+      freqs);
+  return e == cudaSuccess ? RA_OK : RA_ERR_CUDA;
 }
 
 ra_status rope_attn_rotary(const ra_rotary* r, int64_t B, int64_t n, int32_t dtype,
@@ -432,8 +445,9 @@ ra_status rope_attn_rotary_bwd(const ra_rotary* r, int64_t B, int64_t n, int32_t
   if (st != RA_OK || !dalpha) return st;
   const int M = (int)(r->rot_dim / 2);
   const TimingScope timed(K_ROTARY_DALPHA, s);
-  rotary_dalpha_kernel<<<(unsigned)M, 128, 0, s>>>(part, parts, M, freqs, dalpha);
-  return cudaGetLastError() == cudaSuccess ? RA_OK : RA_ERR_CUDA;
+  const cudaError_t e = launch_overlapped(rotary_dalpha_kernel, dim3((unsigned)M), 128, 0, s,
+                                          (const double*)part, parts, M, freqs, dalpha);
+  return e == cudaSuccess ? RA_OK : RA_ERR_CUDA;
 }
 
 }  // extern "C"
