@@ -10,20 +10,17 @@
 //     mbarriers) and keeps its own online softmax.  The four warps of a block meet only at the
 //     end of an item.
 //   * A code never becomes its value.  Or-ing four bits into the mantissa of an fp16 constant
-//     gives 1024 + c (bits 0-3) or 64 + c (bits 4-7): a word of eight codes is four operand
-//     registers for one shift and four logic operations.  What the biases and the (step, lo)
-//     pairs add is linear and comes in outside the inner products:
+//     gives 1024 + c (bits 0-3) or 64 + c (bits 4-7), a packed subtraction c - 8, exactly: a
+//     word of eight codes is four operand registers for one shift, four logic operations and
+//     four subtractions.  (Leaving the bias in and taking it off the sums saves the
+//     subtractions, but the tensor cores' fp32 sums do not round to nearest: of 32768 nearly
+//     equal weights the output was 1.4% off, and the log-sum-exp 6e-6.)  What the (step, lo)
+//     pairs add is linear and comes in outside the inner products, with mid = lo + 8 step:
 //   * S^T = K Q^T with mma.sync.m16n8k16: 16 keys are the M rows, the (up to 8 per tile) query
-//     rows the N columns.  The accumulator starts at minus the bias times sum(q), which leaves
-//     q . c exactly; then s = step acc + lo sum(q), per key and group.
+//     rows the N columns; then s = step (q . (c - 8)) + mid sum(q), per key and group.
 //   * P V as O^T = V^T P^T: channels are the M rows, P^T the B operand, scaled by the keys' steps
 //     before it is rounded to fp16 (one copy per group of 64 channels) and turned around in
-//     registers by movmatrix.  The bias is the same multiple of sum(p step) for every channel:
-//     one more product with ones gives that sum as it was rounded, and every kFlush shares it is
-//     taken off the accumulators, before the tensor cores' fp32 sums (which need not round to
-//     nearest) could lose bits to it.  8 more steps are taken off with it and come back in fp32
-//     with the low ends, sum(p (lo + 8 step)): the rounding of p step then multiplies codes
-//     of -8 .. 7 instead of 0 .. 15.
+//     registers by movmatrix; sum(p mid) is kept in fp32.
 //   * Which key or channel sits in which MMA row is free as long as both products agree; it is
 //     chosen so that every shared-memory read is a conflict-free or two-way 4- or 8-byte
 //     access of the cache's plain channel order.
@@ -50,9 +47,10 @@ namespace {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStages = 3;             // ring of a warp, in its 32-token shares of a step
 constexpr float kTau = 2.0f;           // lazy rescale of the running max, log2 units
-constexpr int kFlush = 16;             // shares between two removals of the codes' bias
-constexpr float kBiasEven = 1024.f, kBiasOdd = 64.f, kMid = 8.f;
-constexpr uint32_t kEvenBits = 0x64006400u, kOddBits = 0x54005400u;  // those as fp16 pairs
+constexpr float kMid = 8.f;            // codes enter the products as c - kMid
+// fp16 pairs: 1024 and 64 (a code or-ed into their mantissas adds itself), and those + kMid
+constexpr uint32_t kEvenBits = 0x64006400u, kOddBits = 0x54005400u;
+constexpr uint32_t kEvenMid = 0x64086408u, kOddMid = 0x54805480u;
 
 template <int D, int NT>
 struct RowsCfg {
@@ -104,13 +102,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
 
-// The A registers of two channels: even one 1024 + c, odd one 64 + c, from the low eight bits of
-// each half of x.
+// The A registers of two channels, c - 8 each, from the low eight bits of each half of x.
 __device__ __forceinline__ uint32_t even_codes(uint32_t x) {
-  return and_or(x, 0x000f000fu, kEvenBits);
+  return as_u32(__hsub2(as_half2(and_or(x, 0x000f000fu, kEvenBits)), as_half2(kEvenMid)));
 }
 __device__ __forceinline__ uint32_t odd_codes(uint32_t x) {
-  return and_or(x, 0x00f000f0u, kOddBits);
+  return as_u32(__hsub2(as_half2(and_or(x, 0x00f000f0u, kOddBits)), as_half2(kOddMid)));
 }
 
 template <int D, int NT>
@@ -208,10 +205,9 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
     const int hi_least = token_keys(c, s.w, row0 / G).hi;
 
     // queries as B operands (row n = 8 nt + lane / 4): the channel pairs (i, i + 4) of each
-    // eight, as the codes are unpacked; their sums over each group, plain and times the bias
+    // eight, as the codes are unpacked; and their sums over each group
     uint32_t qb[NT][NG][8];
     float2 qs[NT][NG];
-    float qbias[NT][NG][4];  // as an accumulator's four elements
     bool beyond = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -221,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
           static_cast<const __nv_bfloat16*>(a.q) + (s.w.q0 + token) * a.q_n + hd * a.q_h;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        float even = 0.f, odd = 0.f;
+        float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -249,60 +245,31 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
             const uint32_t x = pack_f16x2_sat(f[e], f[e + 4]);
             const float2 y = __half22float2(as_half2(x));  // as rounded
             qb[nt][g][4 * j + e] = x;
-            if (e % 2 == 0) even += y.x + y.y;
-            else odd += y.x + y.y;
+            sum += y.x + y.y;
           }
         }
-        float sum = even + odd, bias = kBiasEven * even + kBiasOdd * odd;
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        bias += __shfl_xor_sync(0xffffffffu, bias, 1);
-        bias += __shfl_xor_sync(0xffffffffu, bias, 2);
         qs[nt][g] = make_float2(__shfl_sync(0xffffffffu, sum, 8 * t),
                                 __shfl_sync(0xffffffffu, sum, 8 * t + 4));
-        qbias[nt][g][0] = qbias[nt][g][2] = -__shfl_sync(0xffffffffu, bias, 8 * t);
-        qbias[nt][g][1] = qbias[nt][g][3] = -__shfl_sync(0xffffffffu, bias, 8 * t + 4);
       }
     }
     if (beyond) atomicCAS(a.err, 0u, (uint32_t)RA_ERR_RANGE);
 
-    // running maximum (log2 units), sums of p, O; sums of p step as rounded since the last
-    // flush, and of p (lo + 8 step)
-    float m2[NT][2], o[NT][MT][4], ones[NT][NG][4];
-    float2 l[NT], plo[NT][NG];
+    // running maximum (log2 units), sums of p, O without and sums of p mid
+    float m2[NT][2], o[NT][MT][4];
+    float2 l[NT], pmid[NT][NG];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m2[nt][0] = m2[nt][1] = -CUDART_INF_F;
       l[nt] = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        plo[nt][g] = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ones[nt][g][e] = 0.f;
-      }
+      for (int g = 0; g < NG; ++g) pmid[nt][g] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
     }
-    auto flush = [&]() {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float* x = o[nt][4 * g + i];
-            x[0] = fmaf(-kBiasEven - kMid, ones[nt][g][0], x[0]);
-            x[1] = fmaf(-kBiasEven - kMid, ones[nt][g][1], x[1]);
-            x[2] = fmaf(-kBiasOdd - kMid, ones[nt][g][0], x[2]);
-            x[3] = fmaf(-kBiasOdd - kMid, ones[nt][g][1], x[3]);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) ones[nt][g][e] = 0.f;
-        }
-    };
-
     for (int i = i0; i < i1; ++i) {
       if (gave_up) break;
       const int stage = consumed % kStages;
@@ -325,8 +292,10 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
         for (int g = 0; g < NG; ++g) {
           const uint2 wa = lds64(kb + krow * (D / 2) + g * 32 + t * 8);
           const uint2 wb = lds64(kb + (krow + 8) * (D / 2) + g * 32 + t * 8);
-          const float2 pa = __half22float2(as_half2(lds32(pairs + (krow * NG + g) * 4)));
-          const float2 pb = __half22float2(as_half2(lds32(pairs + ((krow + 8) * NG + g) * 4)));
+          float2 pa = __half22float2(as_half2(lds32(pairs + (krow * NG + g) * 4)));
+          float2 pb = __half22float2(as_half2(lds32(pairs + ((krow + 8) * NG + g) * 4)));
+          pa.y = fmaf(kMid, pa.x, pa.y);
+          pb.y = fmaf(kMid, pb.x, pb.y);
           float acc[NT][4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -337,8 +306,7 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               if (j == 0)
-                mma_f16(acc[nt], a0, a1, a2, a3, qb[nt][g][0], qb[nt][g][1], qbias[nt][g][0],
-                        qbias[nt][g][1], qbias[nt][g][2], qbias[nt][g][3]);
+                mma_f16(acc[nt], a0, a1, a2, a3, qb[nt][g][0], qb[nt][g][1], 0.f, 0.f, 0.f, 0.f);
               else
                 mma_f16(acc[nt], a0, a1, a2, a3, qb[nt][g][2 * j], qb[nt][g][2 * j + 1],
                         acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
@@ -405,11 +373,7 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
           }
           l[nt] = fmul2(l[nt], corr);
 #pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            plo[nt][g] = fmul2(plo[nt][g], corr);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) ones[nt][g][e] *= e % 2 ? corr.y : corr.x;
-          }
+          for (int g = 0; g < NG; ++g) pmid[nt][g] = fmul2(pmid[nt][g], corr);
 #pragma unroll
           for (int i2 = 0; i2 < MT; ++i2)
 #pragma unroll
@@ -421,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
       for (int k = 0; k < 2; ++k) {
         const uint32_t vb = st + k * C::BLOCK_BYTES + value_offset(D);
         const uint32_t pairs = vb + code_bytes(D);
-        float2 va[NG], vbp[NG];  // (step, lo + 8 step) of keys krow, krow + 8
+        float2 va[NG], vbp[NG];  // (step, mid) of keys krow, krow + 8
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           va[g] = __half22float2(as_half2(lds32(pairs + (krow * NG + g) * 4)));
@@ -454,15 +418,12 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
           l[nt] = fadd2(l[nt], fadd2(p0, p1));
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
-            plo[nt][g].x = fmaf(p0.x, va[g].y, fmaf(p1.x, vbp[g].y, plo[nt][g].x));
-            plo[nt][g].y = fmaf(p0.y, va[g].y, fmaf(p1.y, vbp[g].y, plo[nt][g].y));
+            pmid[nt][g].x = fmaf(p0.x, va[g].y, fmaf(p1.x, vbp[g].y, pmid[nt][g].x));
+            pmid[nt][g].y = fmaf(p0.y, va[g].y, fmaf(p1.y, vbp[g].y, pmid[nt][g].y));
             pb[nt][g][0] =
                 transpose8(as_u32(__floats2half2_rn(p0.x * va[g].x, p0.y * va[g].x)));
             pb[nt][g][1] =
                 transpose8(as_u32(__floats2half2_rn(p1.x * vbp[g].x, p1.y * vbp[g].x)));
-            mma_f16(ones[nt][g], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u,
-                    pb[nt][g][0], pb[nt][g][1], ones[nt][g][0], ones[nt][g][1], ones[nt][g][2],
-                    ones[nt][g][3]);
           }
         }
 #pragma unroll
@@ -488,18 +449,16 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
           }
         }
       }
-      if (i % kFlush == kFlush - 1) flush();
       __syncwarp();  // every lane has read the stage
       if (next < i1) issue(s, next++);
     }
 
-    // ---- biases off, sum(p lo) in: a group's channels all get the same
-    flush();
+    // ---- sum(p mid) in: a group's channels all get the same
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        float2 x = plo[nt][g];
+        float2 x = pmid[nt][g];
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1)
           x = fadd2(x, make_float2(__shfl_xor_sync(0xffffffffu, x.x, w),

@@ -89,8 +89,7 @@ class Batch:
         """Every row against the float64 oracle.  Tolerance of an element, U = 2^-24:
           stored type: half a step of |o|;
           a score: fp32 products and sums over d channels and the two affine terms of each
-            group, at most (d + 16) U scale sum |q| (|k| + the 136 steps by which the codes are
-            biased in the products) =: ds, which moves p by 2 ds relative (numerator and sum);
+            group, at most (d + 16) U scale sum |q| (|k| + the 8 steps that the codes are moved by) =: ds, which moves p by 2 ds relative (numerator and sum);
           exp2 and the sums of p: 2^-20 relative (2 ulp of ex2.approx, rescales, sums of at
             most 2^11 terms per lane and step in fp32);
           bf16, more than 64 rows per kv head: p and v are rounded to fp16 (2^-11 each; below 2^-14
@@ -98,9 +97,8 @@ class Batch:
             scale sum |q| (2^-11 |k| + 2^-25), added to ds;
           bf16, up to 64 rows: p step is rounded to fp16 (2^-11 relative, 2^-25 below 2^-14) and
             multiplies codes of -8..7: 8 step (2^-11 + L 2^-25 / step) at most, with
-            step <= 2 vmax / 15; the products carry a bias of at most 1024 + 15 of sum(p step)
-            over the 32 MMAs between two flushes, each of which may lose 2^-23 of the sum:
-            32 1039 2^-23 step.
+            step <= 2 vmax / 15; the fp32 sums of the products may lose 2^-23 of themselves with
+            each 16 keys, 8 step at most: L / 16 2^-23 8 step.
         All of it relative to sum_j p_j |v_j|; lse moves by ds + 2^-20 and its own rounding."""
         U, bf = 2.0 ** -24, self.dtype == torch.bfloat16
         q = self.q.double().numpy() if q is None else q
@@ -115,7 +113,7 @@ class Batch:
             wo, wl, mag = ref.attention(q[at], k, v, scale, self.causal, self.window)
             kmax = np.nanmax(abs(k)) if k.size and not np.isnan(k).all() else 0.0
             q1 = abs(q[at]).sum(-1)
-            ds = ((self.d + 16) * U * scale * q1 * kmax * 18)[..., None]
+            ds = ((self.d + 16) * U * scale * q1 * kmax * (1 + 16 / 15))[..., None]
             if bf and n * (self.Hq // self.Hkv) > 64:
                 ds = ds + (scale * q1 * (2.0 ** -11 * kmax + 2.0 ** -25))[..., None]
             vmax = np.nanmax(abs(v)) if v.size and not np.isnan(v).all() else 0.0
@@ -124,7 +122,7 @@ class Batch:
                 tol = tol + 2 * 2.0 ** -11 * mag * 1.01 + L * 2.0 ** -25 * vmax + 2.0 ** -25
             elif bf:
                 step = 2 * vmax / 15 * 1.01
-                tol = tol + step * (8 * 2.0 ** -11 + 32 * 1039 * 2.0 ** -23) + 8 * L * 2.0 ** -25
+                tol = tol + 8 * step * (2.0 ** -11 + L / 16 * 2.0 ** -23) + 8 * L * 2.0 ** -25
             err = abs(o[at] - wo)
             assert np.isfinite(o[at]).all(), (label, b)
             assert (err <= tol).all(), (label, b, float((err / tol).max()))
