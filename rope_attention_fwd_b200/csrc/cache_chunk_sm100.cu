@@ -23,9 +23,21 @@
 // order in which a 32-bit word of codes unpacks two at a time.  Q, K and V all use it, so the
 // scores do not notice and the output's columns are put back when it is written.
 //
-// Numerics: q, k and v enter as fp16 (k, v rounded once from lo + step code; q converted from
-// bf16, clamped and reported as RA_ERR_RANGE beyond 65504), P as fp16, sums in fp32; lazy
-// rescale as in the dense forward (P <= 2^8).  Every wait is bounded.
+// Scores.  k = lo + step code rounded to fp16 would be 2^-12 off per element, which the
+// log-sum-exp shows (1e-5 of it where a row sees few keys).  So K enters as exact products: with
+// mid = lo + 8 step and the step cut into its upper eight and lower three bits, s1 + s2,
+//   q . k = sum_g (q . s1_g (code - 8))_g + (q . s2_g (code - 8))_g + mid_g sum(q)_g
+// where s (code - 8) has at most 11 bits: two fp16 operand tiles instead of one, and one K-step
+// of 16 more columns for the mids and the queries' group sums, each as a high and a low fp16
+// part (hi mh + lo mh + hi ml: 22 bits).  The tensor cores have the time: a step of 256 rows x
+// 128 keys keeps them busy for about 3200 of its 4700 cycles.  K is single-buffered for it (the
+// next tile is unpacked while the softmax of this one runs), V has two stages.
+// (Fractions u0 / u1 for the two groups' steps with one factor per key, which would need one
+// tile, are no better than rounding where the ratio is near a simple fraction.)
+//
+// Numerics otherwise: q as fp16 (converted from bf16, clamped and reported as RA_ERR_RANGE
+// beyond 65504, the sums of 64 channels too), v = lo + step code rounded once to fp16, P as fp16,
+// sums in fp32; lazy rescale as in the dense forward (P <= 2^8).  Every wait is bounded.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
@@ -43,30 +55,33 @@ namespace {
 
 template <int D>
 struct ChunkCfg {
-  static constexpr int NSK = 2, NSV = 2;                  // K and V ring stages
+  static constexpr int NSV = 2;                           // V ring stages (K has one)
   static constexpr int CH = D / 64;                       // 64-channel chunks per row
   static constexpr uint32_t CHUNK = 128u * 128u;          // [128 rows][128 B]
   static constexpr uint32_t TILE = CHUNK * CH;            // [128][D] fp16
   static constexpr uint32_t OFF_Q = 0;                    // tiles a, b
   static constexpr uint32_t OFF_K = 2 * TILE;
-  static constexpr uint32_t OFF_V = OFF_K + NSK * TILE;
-  static constexpr uint32_t OFF_BAR = OFF_V + NSV * TILE;
+  static constexpr uint32_t OFF_V = OFF_K + 2 * TILE;     // K: s1 and s2 products
+  static constexpr uint32_t EXT = 128u * 32u;             // [128 rows][16] fp16
+  static constexpr uint32_t OFF_QX = OFF_V + NSV * TILE;  // the 16 more columns of Q (a, b) ..
+  static constexpr uint32_t OFF_KX = OFF_QX + 2 * EXT;    // .. and of K
+  static constexpr uint32_t OFF_BAR = OFF_KX + EXT;
   static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;  // + alignment slack
   static constexpr uint32_t COL_S = 0, COL_O = 256;
 };
 
 enum ChunkBar {
   B_Q_FULL = 0,   // both tiles' queries are in shared memory; 8 warp arrivals
-  B_K_FULL = 1,   // +stage: unpacked; 4 warp arrivals
-  B_K_EMPTY = 3,  // +stage: the S products that read it are done
-  B_V_FULL = 5,
-  B_V_EMPTY = 7,
-  B_S_FULL = 9,   // +tile
-  B_P_FULL = 11,  // +tile: P written and O rescaled; 4 warp arrivals
-  B_PV_DONE = 13, // +tile
-  B_O_DONE = 15,  // every product of the segment is done
-  B_DRAIN = 16,
-  B_COUNT = 17
+  B_K_FULL = 1,   // unpacked; 4 warp arrivals
+  B_K_EMPTY = 2,  // the S products that read it are done
+  B_V_FULL = 3,   // +stage
+  B_V_EMPTY = 5,  // +stage
+  B_S_FULL = 7,   // +tile
+  B_P_FULL = 9,   // +tile: P written and O rescaled; 4 warp arrivals
+  B_PV_DONE = 11, // +tile
+  B_O_DONE = 13,  // every product of the segment is done
+  B_DRAIN = 14,
+  B_COUNT = 15
 };
 
 constexpr int kThreads = 512;
@@ -84,6 +99,33 @@ __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t b
 }
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+
+// Codes of eight channels (one 32-bit word) less `base` (0 or 8) as fp16 pairs of channels
+// (i, i + 4): 1024 + code and 64 + code by or-ing, 1024 + base and 64 + base off, all exact.
+template <int BASE>
+__device__ __forceinline__ void unpack8(uint32_t w, __half2 (&v)[4]) {
+  constexpr uint32_t even = BASE ? 0x64086408u : 0x64006400u;
+  constexpr uint32_t odd = BASE ? 0x54805480u : 0x54005400u;
+  static_assert(BASE == 0 || BASE == 8, "the constants above");
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    v[i] = __hsub2(as_half2(and_or(w, 0x000f000fu, 0x64006400u)), as_half2(even));
+    v[i + 1] = __hsub2(as_half2(and_or(w, 0x00f000f0u, 0x54005400u)), as_half2(odd));
+    w >>= 8;
+  }
+}
+
+// x as two fp16 parts.
+struct HiLo {
+  __half hi, lo;
+};
+__device__ __forceinline__ HiLo split(float x) {
+  const __half hi = __float2half_rn(x);
+  return {hi, __float2half_rn(x - __half2float(hi))};
+}
+__device__ __forceinline__ uint32_t pack2(__half a, __half b) {
+  return as_u32(__halves2half2(a, b));
+}
 
 // The steps [j0, j1) of a segment in which row tile x (rows x 128 .. of the item's) sees a key.
 struct StepRange {
@@ -123,8 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
   if (threadIdx.x == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
       const int n = i == B_Q_FULL ? 8
-                    : (i == B_K_FULL || i == B_K_FULL + 1 || i == B_V_FULL ||
-                       i == B_V_FULL + 1 || i == B_P_FULL || i == B_P_FULL + 1)
+                    : (i == B_K_FULL || i == B_V_FULL || i == B_V_FULL + 1 || i == B_P_FULL ||
+                       i == B_P_FULL + 1)
                         ? 4
                         : 1;
       mbar_init(&bar[i], n);
@@ -163,6 +205,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
       constexpr uint32_t idO = idesc_f16_f32(128, D, 0, 1);
       const SDesc dkm = sdesc_split(base_s, 16, 1024);        // K-major tiles
       const SDesc dmn = sdesc_split(base_s, C::CHUNK, 1024);  // V tiles read MN-major
+      // rows of 32 bytes, 32-byte swizzle (layout 6): 256 bytes per 8 rows
+      SDesc dext = sdesc_split(base_s, 16, 256);
+      dext.hi = (dext.hi & ~(7u << 29)) | (6u << 29);
       uint32_t nk = 0, nv = 0, seg = 0;  // K tiles, V tiles and segments so far
       uint32_t np[2] = {0u, 0u};         // P tiles of each row tile so far
       bool ok = true;
@@ -182,32 +227,35 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
           break;
         ++seg;
         tc_fence_after();
-        auto issue_s = [&](int x, uint32_t k) {
-          const SDesc ks = sdesc_advance(dkm, C::OFF_K + (k % C::NSK) * C::TILE);
-          const uint32_t q_off = C::OFF_Q + x * C::TILE;
-          if constexpr (D == 128)
-            mma8_kmajor<false, C::CHUNK, C::CHUNK>(tmem + C::COL_S + x * 128,
-                                                   sdesc_at(dkm, q_off), sdesc_at(ks, 0), idS, 0);
-          else
-            mma4_kmajor<false>(tmem + C::COL_S + x * 128, sdesc_at(dkm, q_off), sdesc_at(ks, 0),
-                               idS, 0);
+        auto issue_s = [&](int x) {
+          const uint32_t d = tmem + C::COL_S + x * 128, q_off = C::OFF_Q + x * C::TILE;
+          mma_ss_warp(d, sdesc_at(dext, C::OFF_QX + x * C::EXT), sdesc_at(dext, C::OFF_KX), idS,
+                      0);
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            const uint32_t k_off = C::OFF_K + part * C::TILE;
+            if constexpr (D == 128)
+              mma8_kmajor<false, C::CHUNK, C::CHUNK>(d, sdesc_at(dkm, q_off),
+                                                     sdesc_at(dkm, k_off), idS, 1);
+            else
+              mma4_kmajor<false>(d, sdesc_at(dkm, q_off), sdesc_at(dkm, k_off), idS, 1);
+          }
           mma_commit_warp(&bar[B_S_FULL + x]);
         };
-        auto wait_k = [&](uint32_t k) -> bool {
-          if (!mbar_wait_warp(&bar[B_K_FULL + k % C::NSK], (k / C::NSK) & 1, abort_flag, a.err,
-                              KID, 2, a.wait_ns))
+        auto wait_k = [&]() -> bool {
+          if (!mbar_wait_warp(&bar[B_K_FULL], nk & 1, abort_flag, a.err, KID, 2, a.wait_ns))
             return false;
           tc_fence_after();
           return true;
         };
-        if (!(ok = wait_k(nk))) break;
+        if (!(ok = wait_k())) break;
         for (int x = 0; x < 2; ++x)
-          if (active(x, j0)) issue_s(x, nk);
-        mma_commit_warp(&bar[B_K_EMPTY + nk % C::NSK]);
+          if (active(x, j0)) issue_s(x);
+        mma_commit_warp(&bar[B_K_EMPTY]);
         ++nk;
         for (int j = j0; ok && j < j1; ++j) {
           const bool next = j + 1 < j1;
-          if (next && !(ok = wait_k(nk))) break;
+          bool have_k = false;  // K(j + 1) has been waited for
           if (!(ok = mbar_wait_warp(&bar[B_V_FULL + nv % C::NSV], (nv / C::NSV) & 1, abort_flag,
                                     a.err, KID, 3, a.wait_ns)))
             break;
@@ -223,13 +271,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
                          idO, j > (x == 0 ? ra_.j0 : rb.j0));
               mma_commit_warp(&bar[B_PV_DONE + x]);
             }
-            if (next && active(x, j + 1)) issue_s(x, nk);
+            if (next && active(x, j + 1)) {
+              if (!have_k && !(ok = wait_k())) break;
+              have_k = true;
+              issue_s(x);
+            }
           }
           if (!ok) break;
           mma_commit_warp(&bar[B_V_EMPTY + nv % C::NSV]);
           ++nv;
           if (next) {
-            mma_commit_warp(&bar[B_K_EMPTY + nk % C::NSK]);
+            mma_commit_warp(&bar[B_K_EMPTY]);
             ++nk;
           }
         }
@@ -281,23 +333,49 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
 #pragma unroll
         for (int g = 0; g < NG; ++g) pairs[z][g] = p[g];
       };
-      auto unpack = [&](int z, uint32_t tile) {  // into the tile at shared address `tile`
+      auto word = [&](int z, int i) {  // 32-bit word i of the row's codes
+        const uint4 w4 = codes[z][i / 4];
+        return i % 4 == 0 ? w4.x : i % 4 == 1 ? w4.y : i % 4 == 2 ? w4.z : w4.w;
+      };
+      auto unpack_k = [&]() {
+        uint32_t x[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};  // the key's 16 more columns
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const __half2 step = as_half2(__byte_perm(pairs[z][g], 0, 0x1010)),
-                        lo = as_half2(__byte_perm(pairs[z][g], 0, 0x3232));
+          const uint32_t pr = pairs[0][g];
+          const __half2 step = as_half2(__byte_perm(pr, 0, 0x1010));
+          const __half2 s1 = as_half2(as_u32(step) & 0xfff8fff8u), s2 = __hsub2(step, s1);
+          const float2 f = __half22float2(as_half2(pr));
+          const HiLo m = split(fmaf(8.f, f.x, f.y));
+          x[2 * g] = pack2(m.hi, m.hi);  // against (hi, lo, hi, -) of the group sum
+          x[2 * g + 1] = pack2(m.lo, __ushort_as_half(0));
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            const uint4 w4 = codes[z][g * 2 + u / 4];
-            const uint32_t w = u % 4 == 0 ? w4.x : u % 4 == 1 ? w4.y : u % 4 == 2 ? w4.z : w4.w;
-            uint32_t v[4];
+            __half2 v[4];
+            unpack8<8>(word(0, g * 8 + u), v);
+            const uint32_t at = base_s + C::OFF_K + g * C::CHUNK + row_off + ((u ^ (key_t & 7)) << 4);
+            st_shared_v4(at, as_u32(__hmul2(v[0], s1)), as_u32(__hmul2(v[1], s1)),
+                         as_u32(__hmul2(v[2], s1)), as_u32(__hmul2(v[3], s1)));
+            st_shared_v4(at + C::TILE, as_u32(__hmul2(v[0], s2)), as_u32(__hmul2(v[1], s2)),
+                         as_u32(__hmul2(v[2], s2)), as_u32(__hmul2(v[3], s2)));
+          }
+        }
+        const uint32_t row = base_s + C::OFF_KX + key_t * 32u, flip = (key_t >> 2 & 1) << 4;
+        st_shared_v4(row + flip, x[0], x[1], x[2], x[3]);
+        st_shared_v4(row + (16u ^ flip), 0u, 0u, 0u, 0u);
+      };
+      auto unpack_v = [&](uint32_t tile) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __half2 cd = as_half2(and_or(w >> (4 * i), 0x000f000fu, 0x64006400u));
-              v[i] = as_u32(__hfma2(__hsub2(cd, as_half2(0x64006400u)), step, lo));
-            }
-            st_shared_v4(tile + g * C::CHUNK + row_off + ((u ^ (key_t & 7)) << 4), v[0], v[1],
-                         v[2], v[3]);
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t pr = pairs[1][g];
+          const __half2 step = as_half2(__byte_perm(pr, 0, 0x1010)),
+                        lo = as_half2(__byte_perm(pr, 0, 0x3232));
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            __half2 v[4];
+            unpack8<0>(word(1, g * 8 + u), v);
+            st_shared_v4(tile + g * C::CHUNK + row_off + ((u ^ (key_t & 7)) << 4),
+                         as_u32(__hfma2(v[0], step, lo)), as_u32(__hfma2(v[1], step, lo)),
+                         as_u32(__hfma2(v[2], step, lo)), as_u32(__hfma2(v[3], step, lo)));
           }
         }
       };
@@ -305,20 +383,20 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
       load(0, j0, page);
       load(1, j0, page);
       for (int j = j0; j < j1; ++j) {
-        const uint32_t sk = nk % C::NSK, sv = nv % C::NSV;
-        if (!(ok = mbar_wait_warp(&bar[B_K_EMPTY + sk], ((nk / C::NSK) & 1) ^ 1, abort_flag, a.err,
-                                  KID, 6, a.wait_ns)))
+        const uint32_t sv = nv % C::NSV;
+        if (!(ok = mbar_wait_warp(&bar[B_K_EMPTY], (nk & 1) ^ 1, abort_flag, a.err, KID, 6,
+                                  a.wait_ns)))
           break;
-        unpack(0, base_s + C::OFF_K + sk * C::TILE);
+        unpack_k();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[B_K_FULL + sk]);
+        if (lane == 0) mbar_arrive(&bar[B_K_FULL]);
         ++nk;
         if (j + 1 < j1) load(0, j + 1, page_next);
         if (!(ok = mbar_wait_warp(&bar[B_V_EMPTY + sv], ((nv / C::NSV) & 1) ^ 1, abort_flag, a.err,
                                   KID, 7, a.wait_ns)))
           break;
-        unpack(1, base_s + C::OFF_V + sv * C::TILE);
+        unpack_v(base_s + C::OFF_V + sv * C::TILE);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar[B_V_FULL + sv]);
@@ -336,8 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
     const uint32_t lane_base = tmem + ((uint32_t)((warp % 4) * 32) << 16);
     const uint32_t s_base = lane_base + C::COL_S + x * 128;
     const uint32_t o_base = lane_base + C::COL_O + x * 128;
-    const float scale_log2 = c.scale * 1.4426950408889634f;
     uint32_t ns = 0, seg = 0;          // S tiles of this row tile, segments with products so far
+    const float scale_log2 = c.scale * 1.4426950408889634f;
     int followers = 0, fb = 0, fh = 0, ft = 0;
     bool ok = true;
     while (ok && walk.next(s)) {
@@ -362,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
         const __nv_bfloat16* src =
             static_cast<const __nv_bfloat16*>(a.q) + token * a.q_n + head * a.q_h;
         bool beyond = false;
+        float sum[NG] = {};
 #pragma unroll 4
         for (int u = 0; u < D / 8; ++u) {
           uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -382,11 +461,28 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
             f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) beyond = beyond || !(fabsf(f[e]) <= 65504.f);
+          for (int e = 0; e < 8; ++e) {
+            beyond = beyond || !(fabsf(f[e]) <= 65504.f);
+            if (NG == 1 || u < 8) sum[0] += f[e];
+            else sum[NG - 1] += f[e];
+          }
           st_shared_v4(tile + (u / 8) * C::CHUNK + (((u % 8) ^ (t & 7)) << 4),
                        pack_f16x2_sat(f[0], f[4]), pack_f16x2_sat(f[1], f[5]),
                        pack_f16x2_sat(f[2], f[6]), pack_f16x2_sat(f[3], f[7]));
         }
+        // the row's 16 more columns: per group (hi, lo, hi, 0) of its sum
+        uint32_t ext[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          beyond = beyond || !(fabsf(sum[g]) <= 65504.f);
+          const HiLo q = split(fminf(fmaxf(sum[g], -65504.f), 65504.f));
+          ext[2 * g] = pack2(q.hi, q.lo);
+          ext[2 * g + 1] = pack2(q.hi, __ushort_as_half(0));
+        }
+        const uint32_t erow = base_s + C::OFF_QX + x * C::EXT + t * 32u;
+        const uint32_t flip = (t >> 2 & 1) << 4;
+        st_shared_v4(erow + flip, ext[0], ext[1], ext[2], ext[3]);
+        st_shared_v4(erow + (16u ^ flip), 0u, 0u, 0u, 0u);
         if (beyond) atomicCAS(a.err, 0u, (uint32_t)RA_ERR_RANGE);
         fence_proxy_async_smem();
         __syncwarp();
@@ -435,7 +531,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
         }
         const float mt = fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]),
                                fmaxf(mp[6], mp[7])) * scale_log2;
-        // scale may be negative or zero in principle: the maximum is taken of the products
         const bool rescale = __any_sync(0xffffffffu, mt > m + kTau);
         if (rescale) {
           const float mn = fmaxf(m, mt);

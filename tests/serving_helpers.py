@@ -93,8 +93,7 @@ class Batch:
           exp2 and the sums of p: 2^-20 relative (2 ulp of ex2.approx, rescales, sums of at
             most 2^11 terms per lane and step in fp32);
           bf16, more than 64 rows per kv head: p and v are rounded to fp16 (2^-11 each; below 2^-14
-            by at most 2^-25 absolute), k too, which moves a score by at most
-            scale sum |q| (2^-11 |k| + 2^-25), added to ds;
+            by at most 2^-25 absolute);
           bf16, up to 64 rows: p step is rounded to fp16 (2^-11 relative, 2^-25 below 2^-14) and
             multiplies codes of -8..7: 8 step (2^-11 + L 2^-25 / step) at most, with
             step <= 2 vmax / 15; the fp32 sums of the products may lose 2^-23 of themselves with
@@ -114,8 +113,6 @@ class Batch:
             kmax = np.nanmax(abs(k)) if k.size and not np.isnan(k).all() else 0.0
             q1 = abs(q[at]).sum(-1)
             ds = ((self.d + 16) * U * scale * q1 * kmax * (1 + 16 / 15))[..., None]
-            if bf and n * (self.Hq // self.Hkv) > 64:
-                ds = ds + (scale * q1 * (2.0 ** -11 * kmax + 2.0 ** -25))[..., None]
             vmax = np.nanmax(abs(v)) if v.size and not np.isnan(v).all() else 0.0
             tol = torch.finfo(self.dtype).eps / 2 * abs(wo) + (2 * ds + 2.0 ** -20) * mag + 1e-30
             if bf and n * (self.Hq // self.Hkv) > 64:
