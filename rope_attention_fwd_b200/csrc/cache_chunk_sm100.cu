@@ -13,9 +13,12 @@
 //   warps 0-3 / 4-7   softmax of tile a / b: thread = row = TMEM lane, the row's 128 scores in
 //                     registers; they also load and convert the queries and write the output
 //   warps 8-11        unpack: thread = key; codes prefetched into registers one tile ahead,
-//                     lo + step code as fp16 into the 128-byte-swizzled operand tiles
+//                     written as fp16 into the 128-byte-swizzled operand tiles
 //   warp 12           TMEM allocator + tcgen05.mma issuer (converged warp, one elected lane)
-//   warps 13-15       idle (they complete the warpgroup that setmaxnreg acts on)
+//   warp 13           walks the run and hands the other roles one segment after the other
+//                     through a ring in shared memory, so that its state (and the divisions)
+//                     take none of their registers; it also looks over the segment's pages
+//   warps 14-15       idle (they complete the warpgroup that setmaxnreg acts on)
 // TMEM (512 columns): S_x at 128 x, P_x (fp16, two per column) over its first 64, O_x at
 // 256 + 128 x.  Issue order as in the dense forward: PV_x(j), then S_x(j + 1), tile by tile.
 //
@@ -23,17 +26,16 @@
 // order in which a 32-bit word of codes unpacks two at a time.  Q, K and V all use it, so the
 // scores do not notice and the output's columns are put back when it is written.
 //
-// Scores.  k = lo + step code rounded to fp16 would be 2^-12 off per element, which the
-// log-sum-exp shows (1e-5 of it where a row sees few keys).  So K enters as exact products: with
-// mid = lo + 8 step and the step cut into its upper eight and lower three bits, s1 + s2,
-//   q . k = sum_g (q . s1_g (code - 8))_g + (q . s2_g (code - 8))_g + mid_g sum(q)_g
-// where s (code - 8) has at most 11 bits: two fp16 operand tiles instead of one, and one K-step
-// of 16 more columns for the mids and the queries' group sums, each as a high and a low fp16
-// part (hi mh + lo mh + hi ml: 22 bits).  The tensor cores have the time: a step of 256 rows x
-// 128 keys keeps them busy for about 3200 of its 4700 cycles.  K is single-buffered for it (the
-// next tile is unpacked while the softmax of this one runs), V has two stages.
-// (Fractions u0 / u1 for the two groups' steps with one factor per key, which would need one
-// tile, are no better than rounding where the ratio is near a simple fraction.)
+// Scores.  With mid = lo + 8 step,
+//   q . k = sum_g (q . step_g (code - 8))_g + mid_g sum(q)_g
+// where the mids and the queries' group sums are one K-step of 16 more columns, each as a high
+// and a low fp16 part (hi mh + lo mh + hi ml: 22 bits).  step (code - 8) has up to 14 bits.
+// Rounded to fp16 it moves a score by 2^-13 of the terms, which the log-sum-exp shows where a
+// row sees few keys (1e-5 of it; over 4096 keys of like weight 3e-7).  So where the tile's first
+// row sees fewer than kExactKeys keys the step is cut into its upper eight and lower three bits,
+// s1 + s2: s (code - 8) then has at most 11 bits, and K is two exact operand tiles instead of
+// one.  Exact products take a fifth more time (2048 tokens over 8192, 32 heads of 128 on 8:
+// 650 us against 541): operands from shared memory saturate its bandwidth.
 //
 // Numerics otherwise: q as fp16 (converted from bf16, clamped and reported as RA_ERR_RANGE
 // beyond 65504, the sums of 64 channels too), v = lo + step code rounded once to fp16, P as fp16,
@@ -43,6 +45,7 @@
 #include <math_constants.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "cache_attn.h"
 #include "cache_sched.cuh"
@@ -55,37 +58,40 @@ namespace {
 
 template <int D>
 struct ChunkCfg {
-  static constexpr int NSV = 2;                           // V ring stages (K has one)
+  static constexpr int NSK = 2, NSV = 2;                  // K and V ring stages
   static constexpr int CH = D / 64;                       // 64-channel chunks per row
   static constexpr uint32_t CHUNK = 128u * 128u;          // [128 rows][128 B]
   static constexpr uint32_t TILE = CHUNK * CH;            // [128][D] fp16
   static constexpr uint32_t OFF_Q = 0;                    // tiles a, b
   static constexpr uint32_t OFF_K = 2 * TILE;
-  static constexpr uint32_t OFF_V = OFF_K + 2 * TILE;     // K: s1 and s2 products
+  static constexpr uint32_t OFF_V = OFF_K + NSK * TILE;
   static constexpr uint32_t EXT = 128u * 32u;             // [128 rows][16] fp16
   static constexpr uint32_t OFF_QX = OFF_V + NSV * TILE;  // the 16 more columns of Q (a, b) ..
-  static constexpr uint32_t OFF_KX = OFF_QX + 2 * EXT;    // .. and of K
-  static constexpr uint32_t OFF_BAR = OFF_KX + EXT;
+  static constexpr uint32_t OFF_KX = OFF_QX + 2 * EXT;    // .. and of K, per stage
+  static constexpr uint32_t OFF_BAR = OFF_KX + NSK * EXT;
   static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;  // + alignment slack
   static constexpr uint32_t COL_S = 0, COL_O = 256;
 };
 
 enum ChunkBar {
   B_Q_FULL = 0,   // both tiles' queries are in shared memory; 8 warp arrivals
-  B_K_FULL = 1,   // unpacked; 4 warp arrivals
-  B_K_EMPTY = 2,  // the S products that read it are done
-  B_V_FULL = 3,   // +stage
-  B_V_EMPTY = 5,  // +stage
-  B_S_FULL = 7,   // +tile
-  B_P_FULL = 9,   // +tile: P written and O rescaled; 4 warp arrivals
-  B_PV_DONE = 11, // +tile
-  B_O_DONE = 13,  // every product of the segment is done
-  B_DRAIN = 14,
-  B_COUNT = 15
+  B_K_FULL = 1,   // +stage: unpacked; 4 warp arrivals
+  B_K_EMPTY = 3,  // +stage: the S products that read it are done
+  B_V_FULL = 5,
+  B_V_EMPTY = 7,
+  B_S_FULL = 9,   // +tile
+  B_P_FULL = 11,  // +tile: P written and O rescaled; 4 warp arrivals
+  B_PV_DONE = 13, // +tile
+  B_O_DONE = 15,  // every product of the segment is done
+  B_DRAIN = 16,
+  B_SEG_FULL = 17,   // +slot
+  B_SEG_EMPTY = 21,  // +slot; one arrival of each consuming warp
+  B_COUNT = 25
 };
 
 constexpr int kThreads = 512;
-constexpr int kUnpackWarp = 8, kMmaWarp = 12;
+constexpr int kUnpackWarp = 8, kMmaWarp = 12, kWalkWarp = 13;
+constexpr int kSegSlots = 4, kSegUsers = 13;  // 8 softmax, 4 unpack, 1 MMA warps
 constexpr float kTau = 8.0f;
 
 // registers per thread after the redistribution: 256 x 184 + 128 x 88 + 128 x 56 = 65,536
@@ -127,22 +133,45 @@ __device__ __forceinline__ uint32_t pack2(__half a, __half b) {
   return as_u32(__halves2half2(a, b));
 }
 
-// The steps [j0, j1) of a segment in which row tile x (rows x 128 .. of the item's) sees a key.
-struct StepRange {
-  int j0, j1;
+constexpr int kExactKeys = 4096;
+
+// A segment as the roles need it.  Row tile x (rows 128 x .. of the item's) sees keys in the
+// steps [lo[x], hi[x]); [j0, j1) is the union, empty if no row sees a key here.
+struct ChunkSeg {
+  int more;          // 0: the run is over
+  int b, h, L, qn, q0;
+  int row0, rows;    // first row of the item's tile among the sequence's, rows of the tile
+  int key0, j0, j1, lo[2], hi[2];
+  int first, last, followers, tile;
+  int exact;         // scores from exact products (two K stages per step)
+  int bad;           // some page of its steps is outside the cache
 };
-__device__ __forceinline__ StepRange tile_steps(const CacheDims& c, const Segment& s, int x,
-                                                int rows) {
+
+__device__ inline void fill_seg(const CacheDims& c, const Segment& s, ChunkSeg& g) {
   const long long row0 = (long long)s.tile * kChunkTile;
-  if (rows <= 128 * x) return {s.s0, s.s0};
-  const KeyRange f = row_keys(c, s.w, row0 + 128 * x, s.w.G);
-  const KeyRange l = row_keys(c, s.w, row0 + min(rows, 128 * x + 128) - 1, s.w.G);
-  StepRange r{s.s0, s.s1};
-  if (l.hi <= s.key0) return {s.s0, s.s0};
-  r.j1 = min(r.j1, (l.hi - s.key0 + kStep - 1) / kStep);
-  if (f.lo > s.key0) r.j0 = max(r.j0, (f.lo - s.key0) / kStep);
-  if (r.j1 < r.j0) r.j1 = r.j0;
-  return r;
+  g.b = s.b, g.h = s.h, g.L = s.w.L, g.qn = s.w.qn, g.q0 = s.w.q0;
+  g.row0 = (int)row0;
+  g.rows = (int)min((long long)kChunkTile, (long long)s.w.qn * s.w.G - row0);
+  g.key0 = s.key0;
+  g.first = s.first, g.last = s.last, g.followers = s.followers, g.tile = s.tile;
+  g.j0 = g.j1 = s.s0;
+  for (int x = 0; x < 2; ++x) {
+    g.lo[x] = g.hi[x] = s.s0;
+    if (g.rows <= 128 * x) continue;
+    const KeyRange f = row_keys(c, s.w, row0 + 128 * x, s.w.G);
+    const KeyRange l = row_keys(c, s.w, row0 + min(g.rows, 128 * x + 128) - 1, s.w.G);
+    if (l.hi <= s.key0) continue;
+    int a = s.s0, e = min(s.s1, (l.hi - s.key0 + kStep - 1) / kStep);
+    if (f.lo > s.key0) a = max(a, (f.lo - s.key0) / kStep);
+    if (a >= e) continue;
+    g.lo[x] = a, g.hi[x] = e;
+    g.j0 = g.j0 < g.j1 ? min(g.j0, a) : a;
+    g.j1 = max(g.j1, e);
+  }
+  const KeyRange f = row_keys(c, s.w, row0, s.w.G);
+  g.exact = f.hi - f.lo < kExactKeys;
+  g.bad = 0;
+  g.more = 1;
 }
 
 template <int D>
@@ -152,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
   constexpr int NG = D / kGroup;
   extern __shared__ uint8_t smem_raw[];
   __shared__ long long scratch[kThreads / 32 + 4];
+  __shared__ ChunkSeg segs[kSegSlots];
   const uint32_t raw_s = smem_u32(smem_raw);
   const uint32_t base_s = (raw_s + 1023u) & ~1023u;
   uint8_t* base = smem_raw + (base_s - raw_s);
@@ -165,10 +195,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
   if (threadIdx.x == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
       const int n = i == B_Q_FULL ? 8
-                    : (i == B_K_FULL || i == B_V_FULL || i == B_V_FULL + 1 || i == B_P_FULL ||
-                       i == B_P_FULL + 1)
+                    : (i == B_K_FULL || i == B_K_FULL + 1 || i == B_V_FULL ||
+                       i == B_V_FULL + 1 || i == B_P_FULL || i == B_P_FULL + 1)
                         ? 4
-                        : 1;
+                    : i >= B_SEG_EMPTY ? kSegUsers
+                                       : 1;
       mbar_init(&bar[i], n);
     }
     *abort_flag = 0;
@@ -190,11 +221,20 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  Walk<WorkOf> walk(WorkOf{a}, run, c.B);
-  Segment s;
-  auto rows_of = [&](const Segment& g) {
-    return (int)min((long long)kChunkTile,
-                    (long long)g.w.qn * G - (long long)g.tile * kChunkTile);
+  // the consuming roles' side of the segment ring: the n-th segment, or null when the run is
+  // over or something gave up; done(n) gives its slot back
+  uint32_t nseg = 0;
+  auto take = [&]() -> const ChunkSeg* {
+    if (!mbar_wait_warp(&bar[B_SEG_FULL + nseg % kSegSlots], nseg / kSegSlots & 1, abort_flag,
+                        a.err, KID, 11, a.wait_ns))
+      return nullptr;
+    const ChunkSeg* g = &segs[nseg % kSegSlots];
+    return g->more ? g : nullptr;
+  };
+  auto done = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[B_SEG_EMPTY + nseg % kSegSlots]);
+    ++nseg;
   };
 
   if (warp >= kMmaWarp) {
@@ -211,17 +251,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
       uint32_t nk = 0, nv = 0, seg = 0;  // K tiles, V tiles and segments so far
       uint32_t np[2] = {0u, 0u};         // P tiles of each row tile so far
       bool ok = true;
-      while (ok && walk.next(s)) {
-        const int rows = rows_of(s);
-        const StepRange ra_ = tile_steps(c, s, 0, rows), rb = tile_steps(c, s, 1, rows);
-        int j0 = ra_.j0, j1 = ra_.j1;
-        if (rb.j0 < rb.j1) {
-          j0 = j0 < j1 ? min(j0, rb.j0) : rb.j0;
-          j1 = max(j1, rb.j1);
-        }
+      while (ok) {
+        const ChunkSeg* g = take();
+        if (!g) break;
+        const int j0 = g->j0, j1 = g->j1, parts = g->exact ? 2 : 1;  // K stages of a step
+        const int lo0 = g->lo[0], hi0 = g->hi[0], lo1 = g->lo[1], hi1 = g->hi[1];
+        done();
         if (j0 >= j1) continue;
         auto active = [&](int x, int j) {
-          return x == 0 ? j >= ra_.j0 && j < ra_.j1 : j >= rb.j0 && j < rb.j1;
+          return x == 0 ? j >= lo0 && j < hi0 : j >= lo1 && j < hi1;
         };
         if (!(ok = mbar_wait_warp(&bar[B_Q_FULL], seg & 1, abort_flag, a.err, KID, 1, a.wait_ns)))
           break;
@@ -229,30 +267,34 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
         tc_fence_after();
         auto issue_s = [&](int x) {
           const uint32_t d = tmem + C::COL_S + x * 128, q_off = C::OFF_Q + x * C::TILE;
-          mma_ss_warp(d, sdesc_at(dext, C::OFF_QX + x * C::EXT), sdesc_at(dext, C::OFF_KX), idS,
-                      0);
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            const uint32_t k_off = C::OFF_K + part * C::TILE;
+          mma_ss_warp(d, sdesc_at(dext, C::OFF_QX + x * C::EXT),
+                      sdesc_at(sdesc_advance(dext, nk % C::NSK * C::EXT), C::OFF_KX), idS, 0);
+          for (int part = 0; part < parts; ++part) {
+            const SDesc ks = sdesc_advance(dkm, (nk + part) % C::NSK * C::TILE);
             if constexpr (D == 128)
               mma8_kmajor<false, C::CHUNK, C::CHUNK>(d, sdesc_at(dkm, q_off),
-                                                     sdesc_at(dkm, k_off), idS, 1);
+                                                     sdesc_at(ks, C::OFF_K), idS, 1);
             else
-              mma4_kmajor<false>(d, sdesc_at(dkm, q_off), sdesc_at(dkm, k_off), idS, 1);
+              mma4_kmajor<false>(d, sdesc_at(dkm, q_off), sdesc_at(ks, C::OFF_K), idS, 1);
           }
           mma_commit_warp(&bar[B_S_FULL + x]);
         };
+        auto release_k = [&]() {
+          for (int part = 0; part < parts; ++part, ++nk)
+            mma_commit_warp(&bar[B_K_EMPTY + nk % C::NSK]);
+        };
         auto wait_k = [&]() -> bool {
-          if (!mbar_wait_warp(&bar[B_K_FULL], nk & 1, abort_flag, a.err, KID, 2, a.wait_ns))
-            return false;
+          for (int part = 0; part < parts; ++part)
+            if (!mbar_wait_warp(&bar[B_K_FULL + (nk + part) % C::NSK], (nk + part) / C::NSK & 1,
+                                abort_flag, a.err, KID, 2, a.wait_ns))
+              return false;
           tc_fence_after();
           return true;
         };
         if (!(ok = wait_k())) break;
         for (int x = 0; x < 2; ++x)
           if (active(x, j0)) issue_s(x);
-        mma_commit_warp(&bar[B_K_EMPTY]);
-        ++nk;
+        release_k();
         for (int j = j0; ok && j < j1; ++j) {
           const bool next = j + 1 < j1;
           bool have_k = false;  // K(j + 1) has been waited for
@@ -268,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
               tc_fence_after();
               const SDesc vs = sdesc_advance(dmn, C::OFF_V + (nv % C::NSV) * C::TILE);
               mma8_ts_mn(tmem + C::COL_O + x * 128, tmem + C::COL_S + x * 128, sdesc_at(vs, 0),
-                         idO, j > (x == 0 ? ra_.j0 : rb.j0));
+                         idO, j > (x == 0 ? lo0 : lo1));
               mma_commit_warp(&bar[B_PV_DONE + x]);
             }
             if (next && active(x, j + 1)) {
@@ -280,10 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
           if (!ok) break;
           mma_commit_warp(&bar[B_V_EMPTY + nv % C::NSV]);
           ++nv;
-          if (next) {
-            mma_commit_warp(&bar[B_K_EMPTY]);
-            ++nk;
-          }
+          if (next) release_k();
         }
         if (ok) mma_commit_warp(&bar[B_O_DONE]);
       }
@@ -291,6 +330,36 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
       mma_commit_warp(&bar[B_DRAIN]);
       int dummy = 0;
       mbar_wait_warp(&bar[B_DRAIN], 0, &dummy, a.err, KID, 5, a.wait_ns);
+    } else if (warp == kWalkWarp) {
+      // ------------------------------------------------------------ walks the run
+      Walk<WorkOf> walk(WorkOf{a}, run, c.B);
+      Segment s;
+      bool more = true;
+      for (uint32_t k = 0; more; ++k) {
+        if (!mbar_wait_warp(&bar[B_SEG_EMPTY + k % kSegSlots], (k / kSegSlots & 1) ^ 1, abort_flag,
+                            a.err, KID, 12, a.wait_ns))
+          break;
+        ChunkSeg& g = segs[k % kSegSlots];
+        more = walk.next(s);  // alike in every lane
+        if (lane == 0) {
+          if (more) fill_seg(c, s, g);
+          else g.more = 0;
+        }
+        __syncwarp();
+        if (more) {
+          // the pages of its steps: rows that meet a bad one mask it (it is reported when it is
+          // unpacked)
+          const int end = min(g.key0 + g.j1 * kStep, g.L);
+          bool bad = false;
+          for (int key = g.key0 + g.j0 * kStep + lane * kBlock; key < end; key += 32 * kBlock)
+            bad = bad || !page_ok(c, a.table[(long long)g.b * c.max_pages +
+                                             key / kBlock / c.page_blocks]);
+          bad = __any_sync(0xffffffffu, bad);
+          if (lane == 0) g.bad = bad;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[B_SEG_FULL + k % kSegSlots]);
+      }
     }
   } else if (warp >= kUnpackWarp) {
     // -------------------------------------------------------------- unpack: thread = key
@@ -301,29 +370,27 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
     bool ok = true;
     uint4 codes[2][D / 32];  // [K, V] of the next tile
     uint32_t pairs[2][NG];
-    while (ok && walk.next(s)) {
-      const int rows = rows_of(s);
-      const StepRange r0 = tile_steps(c, s, 0, rows), r1 = tile_steps(c, s, 1, rows);
-      int j0 = r0.j0, j1 = r0.j1;
-      if (r1.j0 < r1.j1) {
-        j0 = j0 < j1 ? min(j0, r1.j0) : r1.j0;
-        j1 = max(j1, r1.j1);
-      }
+    while (ok) {
+      const ChunkSeg* sg = take();
+      if (!sg) break;
+      const int first = sg->key0 + key_t, L = sg->L, b = sg->b, h = sg->h, j0 = sg->j0,
+                j1 = sg->j1, exact = sg->exact;
+      done();
       if (j0 >= j1) continue;
       // page of this thread's key in step j (-1: behind the last token, or a bad page)
       auto page_at = [&](int j) -> int {
-        const int key = s.key0 + j * kStep + key_t;
-        if (j >= j1 || key >= s.w.L) return -1;
-        return page_of(c, a.table, s.b, key / kBlock, a.err, KID);
+        const int key = first + j * kStep;
+        if (j >= j1 || key >= L) return -1;
+        return page_of(c, a.table, b, key / kBlock, a.err, KID);
       };
       auto load = [&](int z, int j, int page) {  // z: 0 K, 1 V
-        const int key = s.key0 + j * kStep + key_t;
+        const int key = first + j * kStep;
 #pragma unroll
         for (int g = 0; g < NG; ++g) pairs[z][g] = 0u;  // masked keys: value 0
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) codes[z][i] = make_uint4(0u, 0u, 0u, 0u);
         if (page < 0) return;
-        const uint8_t* block = a.cache + block_at(c, page, s.h, key / kBlock % c.page_blocks) +
+        const uint8_t* block = a.cache + block_at(c, page, h, key / kBlock % c.page_blocks) +
                                z * value_offset(D);
         const uint4* src = reinterpret_cast<const uint4*>(block + key % kBlock * (D / 2));
 #pragma unroll
@@ -337,13 +404,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
         const uint4 w4 = codes[z][i / 4];
         return i % 4 == 0 ? w4.x : i % 4 == 1 ? w4.y : i % 4 == 2 ? w4.z : w4.w;
       };
-      auto unpack_k = [&]() {
+      auto unpack_k = [&](auto two) {  // into stage nk (exact: and nk + 1)
+        constexpr bool kTwo = decltype(two)::value;
+        const uint32_t t1 = base_s + C::OFF_K + nk % C::NSK * C::TILE;
+        const uint32_t t2 = base_s + C::OFF_K + (nk + 1) % C::NSK * C::TILE;
         uint32_t x[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};  // the key's 16 more columns
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           const uint32_t pr = pairs[0][g];
           const __half2 step = as_half2(__byte_perm(pr, 0, 0x1010));
-          const __half2 s1 = as_half2(as_u32(step) & 0xfff8fff8u), s2 = __hsub2(step, s1);
+          const __half2 s1 = kTwo ? as_half2(as_u32(step) & 0xfff8fff8u) : step;
+          const __half2 s2 = __hsub2(step, s1);
           const float2 f = __half22float2(as_half2(pr));
           const HiLo m = split(fmaf(8.f, f.x, f.y));
           x[2 * g] = pack2(m.hi, m.hi);  // against (hi, lo, hi, -) of the group sum
@@ -352,14 +423,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
           for (int u = 0; u < 8; ++u) {
             __half2 v[4];
             unpack8<8>(word(0, g * 8 + u), v);
-            const uint32_t at = base_s + C::OFF_K + g * C::CHUNK + row_off + ((u ^ (key_t & 7)) << 4);
-            st_shared_v4(at, as_u32(__hmul2(v[0], s1)), as_u32(__hmul2(v[1], s1)),
+            const uint32_t at = g * C::CHUNK + row_off + ((u ^ (key_t & 7)) << 4);
+            st_shared_v4(t1 + at, as_u32(__hmul2(v[0], s1)), as_u32(__hmul2(v[1], s1)),
                          as_u32(__hmul2(v[2], s1)), as_u32(__hmul2(v[3], s1)));
-            st_shared_v4(at + C::TILE, as_u32(__hmul2(v[0], s2)), as_u32(__hmul2(v[1], s2)),
-                         as_u32(__hmul2(v[2], s2)), as_u32(__hmul2(v[3], s2)));
+            if constexpr (kTwo)
+              st_shared_v4(t2 + at, as_u32(__hmul2(v[0], s2)), as_u32(__hmul2(v[1], s2)),
+                           as_u32(__hmul2(v[2], s2)), as_u32(__hmul2(v[3], s2)));
           }
         }
-        const uint32_t row = base_s + C::OFF_KX + key_t * 32u, flip = (key_t >> 2 & 1) << 4;
+        const uint32_t row = base_s + C::OFF_KX + nk % C::NSK * C::EXT + key_t * 32u;
+        const uint32_t flip = (key_t >> 2 & 1) << 4;
         st_shared_v4(row + flip, x[0], x[1], x[2], x[3]);
         st_shared_v4(row + (16u ^ flip), 0u, 0u, 0u, 0u);
       };
@@ -384,14 +457,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
       load(1, j0, page);
       for (int j = j0; j < j1; ++j) {
         const uint32_t sv = nv % C::NSV;
-        if (!(ok = mbar_wait_warp(&bar[B_K_EMPTY], (nk & 1) ^ 1, abort_flag, a.err, KID, 6,
-                                  a.wait_ns)))
-          break;
-        unpack_k();
+        const int parts = exact ? 2 : 1;
+        for (int part = 0; ok && part < parts; ++part)
+          ok = mbar_wait_warp(&bar[B_K_EMPTY + (nk + part) % C::NSK],
+                              ((nk + part) / C::NSK & 1) ^ 1, abort_flag, a.err, KID, 6,
+                              a.wait_ns);
+        if (!ok) break;
+        if (exact) unpack_k(std::true_type{});
+        else unpack_k(std::false_type{});
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[B_K_FULL]);
-        ++nk;
+        for (int part = 0; part < parts; ++part, ++nk)
+          if (lane == 0) mbar_arrive(&bar[B_K_FULL + nk % C::NSK]);
         if (j + 1 < j1) load(0, j + 1, page_next);
         if (!(ok = mbar_wait_warp(&bar[B_V_EMPTY + sv], ((nv / C::NSV) & 1) ^ 1, abort_flag, a.err,
                                   KID, 7, a.wait_ns)))
@@ -416,24 +493,28 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
     const uint32_t o_base = lane_base + C::COL_O + x * 128;
     uint32_t ns = 0, seg = 0;          // S tiles of this row tile, segments with products so far
     const float scale_log2 = c.scale * 1.4426950408889634f;
-    int followers = 0, fb = 0, fh = 0, ft = 0;
+    PartDesc split_item{0, 0, 0, 0};
     bool ok = true;
-    while (ok && walk.next(s)) {
-      const int rows = rows_of(s);
-      const StepRange r0 = tile_steps(c, s, 0, rows), r1 = tile_steps(c, s, 1, rows);
-      const bool any = r0.j0 < r0.j1 || r1.j0 < r1.j1;
-      const StepRange mine = x == 0 ? r0 : r1;
+    while (ok) {
+      const ChunkSeg* sp = take();
+      if (!sp) break;
+      const ChunkSeg& s = *sp;         // given back at the end of the segment
+      const bool any = s.j0 < s.j1;
+      const int mine_lo = s.lo[x], mine_hi = s.hi[x];
       const int r = 128 * x + t;       // row of the item's tile
-      const long long row = (long long)s.tile * kChunkTile + r;
-      const bool live = r < rows;
-      const KeyRange kr = live ? row_keys(c, s.w, row, G) : KeyRange{0, 0};
-      const long long token = s.w.q0 + (live ? row / G : 0);
-      const long long head = (long long)s.h * G + (live ? row % G : 0);
+      const bool live = r < s.rows;
+      SeqWork w{};
+      w.L = s.L, w.qn = s.qn;
+      const int tok = (s.row0 + (live ? r : 0)) / G;
+      const KeyRange kr = live ? token_keys(c, w, tok) : KeyRange{0, 0};
+      const long long token = s.q0 + tok;
+      const long long head = (long long)s.h * G + (s.row0 + (live ? r : 0)) - (long long)tok * G;
       // keys that every live row of the tile sees (both ends rise with the row): a step inside
       // needs no mask
-      const int last_r = max(0, min(rows, 128 * x + 128) - 1);
-      const KeyRange tf = row_keys(c, s.w, (long long)s.tile * kChunkTile + 128 * x, G);
-      const KeyRange tl = row_keys(c, s.w, (long long)s.tile * kChunkTile + last_r, G);
+      const int last_r = max(0, min(s.rows, 128 * x + 128) - 1);
+      const int hi_least = token_keys(c, w, (s.row0 + 128 * x) / G).hi;
+      const int lo_most = token_keys(c, w, (s.row0 + last_r) / G).lo;
+      const int key0 = s.key0, L = s.L, seq = s.b, bad = s.bad;
       if (any) {
         // the row's query as fp16, in the unpacked channel order, into the swizzled tile
         const uint32_t tile = base_s + C::OFF_Q + x * C::TILE + t * 128u;
@@ -491,14 +572,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
       float m = -CUDART_INF_F, l = 0.f;
       // blocks of 16 keys of a step that hold readable keys (bad pages count as masked)
       auto readable = [&](int j) -> uint32_t {
-        const int key = s.key0 + j * kStep + lane * kBlock;
+        const int key = key0 + j * kStep + lane * kBlock;
         const bool good =
-            lane < kStep / kBlock && key < s.w.L &&
-            page_ok(c, a.table[(long long)s.b * c.max_pages + key / kBlock / c.page_blocks]);
-        return __ballot_sync(0xffffffffu, good || lane >= kStep / kBlock || key >= s.w.L);
+            lane < kStep / kBlock && key < L &&
+            page_ok(c, a.table[(long long)seq * c.max_pages + key / kBlock / c.page_blocks]);
+        return __ballot_sync(0xffffffffu, good || lane >= kStep / kBlock || key >= L);
       };
-      for (int j = mine.j0; j < mine.j1; ++j) {
-        const uint32_t blocks = readable(j);
+      for (int j = mine_lo; j < mine_hi; ++j) {
+        const uint32_t blocks = bad ? readable(j) : 0xffffffffu;
         if (!mbar_wait_warp(&bar[B_S_FULL + x], ns & 1, abort_flag, a.err, KID, 8, a.wait_ns)) {
           ok = false;
           break;
@@ -509,8 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
         for (int q = 0; q < 4; ++q) tmem_ld32(s_base + 32 * q, sr[q]);
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_wait_ld(sr[q]);
-        const int k0 = s.key0 + j * kStep;
-        if (k0 < tl.lo || k0 + kStep > tf.hi || blocks != 0xffffffffu) {
+        const int k0 = key0 + j * kStep;
+        if (k0 < lo_most || k0 + kStep > hi_least || blocks != 0xffffffffu) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -537,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
           const float corr = mn == -CUDART_INF_F ? 1.f : fast_exp2(m - mn);
           m = mn;
           l *= corr;
-          if (j > mine.j0) {
+          if (j > mine_lo) {
             // O must hold every product issued so far
             if (!mbar_wait_warp(&bar[B_PV_DONE + x], (ns - 1) & 1, abort_flag, a.err, KID, 9,
                                 a.wait_ns)) {
@@ -591,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
       const bool whole = s.first && s.last;
       const long long slot = 2ll * blockIdx.x + (s.first ? 1 : 0);
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const bool seen = mine.j0 < mine.j1;  // O holds something
+      const bool seen = mine_lo < mine_hi;  // O holds something
       const long long at = whole ? token * c.Hq + head : slot * kChunkTile + r;
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
@@ -630,12 +711,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
           a.ml[at * 2 + 1] = l;
         }
       }
-      if (s.followers) followers = s.followers, fb = s.b, fh = s.h, ft = s.tile;
+      if (s.followers) split_item = PartDesc{s.followers, s.b, s.h, s.tile};
+      done();
       // the next segment's products overwrite O and the queries only after this warp's arrival
       // on its P and Q barriers
       tc_fence_before();
     }
-    if (threadIdx.x == 0) a.desc[blockIdx.x] = PartDesc{ok ? followers : 0, fb, fh, ft};
+    if (threadIdx.x == 0) {
+      if (!ok) split_item.followers = 0;
+      a.desc[blockIdx.x] = split_item;
+    }
   }
 
   tc_fence_before();
