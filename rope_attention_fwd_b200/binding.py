@@ -7,6 +7,7 @@ call fails, a RuntimeError is raised.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -104,7 +105,8 @@ def lib():
         L.rope_attn_device_status.restype = ctypes.c_int
         L.rope_attn_status_string.argtypes = [ctypes.c_int]
         L.rope_attn_status_string.restype = ctypes.c_char_p
-        R, W, C = (ctypes.POINTER(x) for x in (RaRotary, RaRows, RaCache))
+        R, C = (ctypes.POINTER(x) for x in (RaRotary, RaCache))
+        W = vp   # an ra_rows: its bytes, or a pointer
         i64, i32 = ctypes.c_int64, ctypes.c_int32
         L.rope_attn_rotary_freqs.argtypes = [R, vp, vp, vp]
         L.rope_attn_rotary_freqs.restype = ctypes.c_int
@@ -418,22 +420,21 @@ def _vector(fn, name, t, index, dtype, shape):
                      f"on {t.device}")
 
 
+_pack_rows = struct.Struct("=qqqqq").pack    # the fields of ra_rows
+
+
 def _head_rows(fn, name, t, index, dtype, shape):
-    """RaRows of [B, H, n, d] (4 dimensions) or [T, H, d] (3): any strides, channels
-    contiguous."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
-        raise ValueError(f"{fn}: {name} must be {dtype} of shape {tuple(shape)} on device {index}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    st = t.stride()
-    if st[-1] != 1:
+    """The bytes of an ra_rows of [B, H, n, d] (4 dimensions) or [T, H, d] (3): any strides,
+    channels contiguous."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+        st = t.stride()
+        if st[-1] == 1:
+            if len(st) == 4:
+                return _pack_rows(t.data_ptr(), shape[1], st[0], st[1], st[2])
+            return _pack_rows(t.data_ptr(), shape[1], 0, st[1], st[0])
         raise ValueError(f"{fn}: {name} must have contiguous channels, got strides {st}")
-    if len(st) == 4:
-        return RaRows(t.data_ptr(), shape[1], st[0], st[1], st[2])
-    return RaRows(t.data_ptr(), shape[1], 0, st[1], st[0])
-
-
-def _opt(rows):
-    return ctypes.byref(rows) if rows is not None else None
+    raise ValueError(f"{fn}: {name} must be {dtype} of shape {tuple(shape)} on device {index}, got "
+                     f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def rotary_spec(d, base=10000.0, rot_dim=None, layout="interleaved", scaling="none", factor=1.0,
@@ -458,8 +459,8 @@ def rope_attn_rotary_freqs(spec, alpha=None, freqs=None, device=None):
     fn = "rope_attn_rotary_freqs"
     half = spec.rot_dim // 2
     if freqs is None:
-        freqs = torch.empty(half, dtype=torch.float64,
-                            device=alpha.device if alpha is not None else device or "cuda")
+        freqs = alpha.new_empty(half, dtype=torch.float64) if alpha is not None else \
+            torch.empty(half, dtype=torch.float64, device=device or "cuda")
     dev = _serving_device(fn, freqs)
     _call(fn, dev, ctypes.byref(spec),
           None if alpha is None else _vector(fn, "alpha", alpha, dev, torch.float32, (half,)),
@@ -468,20 +469,24 @@ def rope_attn_rotary_freqs(spec, alpha=None, freqs=None, device=None):
 
 
 def _rotary_args(fn, spec, freqs, x, pos):
-    if x.dim() != 4 or x.dtype not in _DTYPE or x.shape[-1] != spec.d:
+    shape, dtype = x.shape, _DTYPE.get(x.dtype)
+    if len(shape) != 4 or dtype is None or shape[3] != spec.d:
         raise ValueError(f"{fn}: tensors must be [B, H, n, {spec.d}] in float32 or bfloat16, got "
-                         f"{x.dtype} {tuple(x.shape)}")
+                         f"{x.dtype} {tuple(shape)}")
     dev = _serving_device(fn, x)
-    B, _, n, _ = x.shape
+    B, _, n, _ = shape
     f = _vector(fn, "freqs", freqs, dev, torch.float64, (spec.rot_dim // 2,))
     p = None if pos is None else _vector(fn, "pos", pos, dev, torch.int32, (B, n))
-    return dev, (ctypes.byref(spec), B, n, _DTYPE[x.dtype], f, p)
+    return dev, (ctypes.byref(spec), B, n, dtype, f, p)
 
 
-def _same_tokens(fn, name, t, x):
-    if t.dim() != 4 or t.shape[0] != x.shape[0] or t.shape[2:] != x.shape[2:]:
+def _same_tokens(fn, name, t, q_shape):
+    """t's shape, which must be q's but for the heads."""
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != q_shape[0] or shape[2:] != q_shape[2:]:
         raise ValueError(f"{fn}: {name} must match q in batch, tokens and channels, got "
-                         f"{tuple(t.shape)} beside {tuple(x.shape)}")
+                         f"{tuple(shape)} beside {tuple(q_shape)}")
+    return shape
 
 
 def rope_attn_rotary(spec, freqs, q, k=None, pos=None, q_out=None, k_out=None):
@@ -489,16 +494,18 @@ def rope_attn_rotary(spec, freqs, q, k=None, pos=None, q_out=None, k_out=None):
     None) rotated at positions pos (int32 [B, n]; None: 0..n-1).  q_out may be q, k_out k."""
     fn = "rope_attn_rotary"
     dev, head = _rotary_args(fn, spec, freqs, q, pos)
+    dt, shape = q.dtype, q.shape
     q_out = torch.empty_like(q) if q_out is None else q_out
-    rows = [_head_rows(fn, "q", q, dev, q.dtype, q.shape),
-            _head_rows(fn, "q_out", q_out, dev, q.dtype, q.shape), None, None]
-    if k is not None:
-        _same_tokens(fn, "k", k, q)
-        k_out = torch.empty_like(k) if k_out is None else k_out
-        rows[2] = _head_rows(fn, "k", k, dev, q.dtype, k.shape)
-        rows[3] = _head_rows(fn, "k_out", k_out, dev, q.dtype, k.shape)
-    _call(fn, dev, *head, *[_opt(r) for r in rows])
-    return q_out, k_out if k is not None else None
+    q_in = _head_rows(fn, "q", q, dev, dt, shape)
+    q_to = _head_rows(fn, "q_out", q_out, dev, dt, shape)
+    if k is None:
+        _call(fn, dev, *head, q_in, q_to, None, None)
+        return q_out, None
+    shape = _same_tokens(fn, "k", k, shape)
+    k_out = torch.empty_like(k) if k_out is None else k_out
+    _call(fn, dev, *head, q_in, q_to, _head_rows(fn, "k", k, dev, dt, shape),
+          _head_rows(fn, "k_out", k_out, dev, dt, shape))
+    return q_out, k_out
 
 
 def rope_attn_rotary_workspace_bytes(spec):
@@ -511,15 +518,15 @@ def rope_attn_rotary_bwd(spec, freqs, dq_rot, dk_rot=None, q=None, k=None, pos=N
     forward's inputs) are needed for dalpha only; frozen_alpha: None is returned in its place."""
     fn = "rope_attn_rotary_bwd"
     dev, head = _rotary_args(fn, spec, freqs, dq_rot, pos)
-    dt = dq_rot.dtype
+    dt, q_shape, k_shape = dq_rot.dtype, dq_rot.shape, None
     dq = torch.empty_like(dq_rot) if dq is None else dq
-    rows = [_head_rows(fn, "dq_rot", dq_rot, dev, dt, dq_rot.shape),
-            _head_rows(fn, "dq", dq, dev, dt, dq_rot.shape), None, None, None, None]
+    rows = [_head_rows(fn, "dq_rot", dq_rot, dev, dt, q_shape),
+            _head_rows(fn, "dq", dq, dev, dt, q_shape), None, None, None, None]
     if dk_rot is not None:
-        _same_tokens(fn, "dk_rot", dk_rot, dq_rot)
+        k_shape = _same_tokens(fn, "dk_rot", dk_rot, q_shape)
         dk = torch.empty_like(dk_rot) if dk is None else dk
-        rows[2] = _head_rows(fn, "dk_rot", dk_rot, dev, dt, dk_rot.shape)
-        rows[3] = _head_rows(fn, "dk", dk, dev, dt, dk_rot.shape)
+        rows[2] = _head_rows(fn, "dk_rot", dk_rot, dev, dt, k_shape)
+        rows[3] = _head_rows(fn, "dk", dk, dev, dt, k_shape)
     out, w, nbytes = None, None, 0
     if frozen_alpha:
         dalpha = None
@@ -527,19 +534,18 @@ def rope_attn_rotary_bwd(spec, freqs, dq_rot, dk_rot=None, q=None, k=None, pos=N
         if q is None or (k is None) != (dk_rot is None):
             raise ValueError(f"{fn}: dalpha needs the forward's q (and k, if it had one); pass "
                              "frozen_alpha=True for none")
-        rows[4] = _head_rows(fn, "q", q, dev, dt, dq_rot.shape)
+        rows[4] = _head_rows(fn, "q", q, dev, dt, q_shape)
         if dk_rot is not None:
-            rows[5] = _head_rows(fn, "k", k, dev, dt, dk_rot.shape)
+            rows[5] = _head_rows(fn, "k", k, dev, dt, k_shape)
         half = spec.rot_dim // 2
         if dalpha is None:
-            dalpha = torch.empty(half, dtype=torch.float32, device=dq.device)
+            dalpha = freqs.new_empty(half, dtype=torch.float32)
         out = _vector(fn, "dalpha", dalpha, dev, torch.float32, (half,))
         if ws is None:
-            ws = torch.empty(rope_attn_rotary_workspace_bytes(spec), dtype=torch.uint8,
-                             device=dq.device)
+            ws = freqs.new_empty(rope_attn_rotary_workspace_bytes(spec), dtype=torch.uint8)
         nbytes = ws.numel()
         w = _vector(fn, "ws", ws, dev, torch.uint8, (nbytes,))
-    _call(fn, dev, *head, *[_opt(r) for r in rows], out, w, nbytes)
+    _call(fn, dev, *head, *rows, out, w, nbytes)
     return dq, dk if dk_rot is not None else None, dalpha
 
 
@@ -622,7 +628,7 @@ def rope_attn_cache_append(plan, cache, table, indptr, kv_len, spec, freqs, k, v
         rows[2] = _head_rows(fn, "q", q, dev, dt, qs)
         q_out = torch.empty_like(q) if q_out is None else q_out
         rows[3] = _head_rows(fn, "q_out", q_out, dev, dt, qs)
-    _call(fn, dev, *head, ctypes.byref(spec), f, *[_opt(r) for r in rows], *tail)
+    _call(fn, dev, *head, ctypes.byref(spec), f, *rows, *tail)
     return q_out if q is not None else None
 
 
@@ -633,9 +639,10 @@ def rope_attn_cache_read(plan, cache, table, indptr, kv_len, k=None, v=None, ws=
     dev, head, tail, dt = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)
     kv = (plan.T, plan.Hkv, plan.d)
     k = cache.new_empty(kv, dtype=dt) if k is None else k
-    v = cache.new_empty(kv, dtype=dt) if v is None else v
+    if v is None:
+        v = torch.empty_like(k) if k.is_contiguous() else cache.new_empty(kv, dtype=dt)
     rows = [_head_rows(fn, "k", k, dev, dt, kv), _head_rows(fn, "v", v, dev, dt, kv)]
-    _call(fn, dev, *head, ctypes.byref(rows[0]), ctypes.byref(rows[1]), *tail)
+    _call(fn, dev, *head, rows[0], rows[1], *tail)
     return k, v
 
 
@@ -647,9 +654,10 @@ def rope_attn_cache_attn(plan, cache, table, indptr, kv_len, q, o=None, lse=None
     T, Hq = plan.T, plan.Hq
     qs = (T, Hq, plan.d)
     rows = _head_rows(fn, "q", q, dev, dt, qs)
-    o = q.new_empty(qs) if o is None else o
+    if o is None:
+        o = torch.empty_like(q) if q.is_contiguous() else q.new_empty(qs)
     lse = q.new_empty((T, Hq), dtype=torch.float32) if lse is None else lse
-    _call(fn, dev, *head, ctypes.byref(rows), _vector(fn, "o", o, dev, dt, qs),
+    _call(fn, dev, *head, rows, _vector(fn, "o", o, dev, dt, qs),
           _vector(fn, "lse", lse, dev, torch.float32, (T, Hq)), *tail)
     return o, lse
 
