@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const __gri
 
   grid_wait();
   const Run run = find_run(a, scratch, K_CACHE_ATTN_F32);
-  Walk<WorkOf> walk(WorkOf{a}, run, c.B);
+  Walk<WorkOf> walk(WorkOf{a}, run, c.B, c.Hkv);
   Segment s;
   int followers = 0, fb = 0, fh = 0, ft = 0;
   while (walk.next(s)) {
@@ -426,6 +426,7 @@ ra_status rope_attn_cache_attn(const ra_cache* p, const void* cache, const int32
   a.min_steps = 2;
   const size_t rows_end = partials(a, kCacheErrBytes, kRowsBlocks, kRowsTile);
   if (p->dtype == RA_F32) {
+    a.min_steps = 1;
     const TimingScope timed(K_CACHE_ATTN_F32, s);
     const int rows = (int)std::min<int64_t>(most_rows, 8);
     ca.blocks[0] = kRowsBlocks;

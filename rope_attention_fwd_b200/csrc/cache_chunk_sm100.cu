@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attn_chunk_kernel(const __g
       mbar_wait_warp(&bar[B_DRAIN], 0, &dummy, a.err, KID, 5, a.wait_ns);
     } else if (warp == kWalkWarp) {
       // ------------------------------------------------------------ walks the run
-      Walk<WorkOf> walk(WorkOf{a}, run, c.B);
+      Walk<WorkOf> walk(WorkOf{a}, run, c.B, c.Hkv);
       Segment s;
       bool more = true;
       for (uint32_t k = 0; more; ++k) {

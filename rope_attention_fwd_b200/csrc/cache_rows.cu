@@ -178,9 +178,35 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
       bulk_load(ring + stage * C::STAGE + mine * C::BLOCK_BYTES, ad, C::BLOCK_BYTES,
                 &bar[stage]);
   };
-  // take up segment s and begin its copies (the ring is empty)
+  // the current segment's queries as they lie in memory: row n = 8 nt + lane / 4, the channels
+  // 64 g + 16 t + 8 j ..
+  uint4 qw[NT][NG][2];
+  // take up segment s: begin its copies (the ring is empty) and the loads of its queries
   auto begin = [&](const Segment& s) {
     const int row0 = s.tile * TILE, rows = min(TILE, s.w.qn * G - row0);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int n = 8 * nt + r, token = (row0 + n) / G, hd = s.h * G + (row0 + n) - token * G;
+      const __nv_bfloat16* src =
+          static_cast<const __nv_bfloat16*>(a.q) + (s.w.q0 + token) * a.q_n + hd * a.q_h;
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (n < rows) {
+            const __nv_bfloat16* p = src + g * kGroup + 16 * t + 8 * j;
+            if (a.q_vec) {
+              v = *reinterpret_cast<const uint4*>(p);
+            } else {
+              const uint16_t* x = reinterpret_cast<const uint16_t*>(p);
+              v = make_uint4(x[0] | (uint32_t)x[1] << 16, x[2] | (uint32_t)x[3] << 16,
+                             x[4] | (uint32_t)x[5] << 16, x[6] | (uint32_t)x[7] << 16);
+            }
+          }
+          qw[nt][g][j] = v;
+        }
+    }
     const KeyRange kf = token_keys(c, s.w, row0 / G);
     const KeyRange kl = token_keys(c, s.w, (row0 + rows - 1) / G);
     base = s.key0 + warp * 32;
@@ -211,27 +237,12 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
     bool beyond = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int n = 8 * nt + r;
-      const int token = (row0 + n) / G, hd = s.h * G + (row0 + n) - token * G;
-      const __nv_bfloat16* src =
-          static_cast<const __nv_bfloat16*>(a.q) + (s.w.q0 + token) * a.q_n + hd * a.q_h;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          uint32_t w[4] = {0u, 0u, 0u, 0u};
-          if (n < rows) {
-            const __nv_bfloat16* p = src + g * kGroup + 16 * t + 8 * j;
-            if (a.q_vec) {
-              const uint4 v = *reinterpret_cast<const uint4*>(p);
-              w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-            } else {
-              const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) w[e] = h[2 * e] | ((uint32_t)h[2 * e + 1] << 16);
-            }
-          }
+          const uint32_t w[4] = {qw[nt][g][j].x, qw[nt][g][j].y, qw[nt][g][j].z, qw[nt][g][j].w};
           float f[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {

@@ -77,6 +77,7 @@ __device__ inline Run find_run(const AttnArgs& a, long long* scratch, int kid) {
   }
   Run r;
   r.per = steps_per_block(total, (int)gridDim.x, a.min_steps);
+  r.whole = whole_steps(r.per, a.tile);
   r.begin = min(total, (long long)blockIdx.x * r.per);
   r.end = min(total, r.begin + r.per);
   r.b = 0;
@@ -111,7 +112,7 @@ struct SharedWalk {
   int more[2];
 
   __device__ void start(const AttnArgs& a, const Run& r) {
-    new (&walk) Walk<WorkOf>(WorkOf{a}, r, a.c.B);
+    new (&walk) Walk<WorkOf>(WorkOf{a}, r, a.c.B, a.c.Hkv);
     advance(0);
   }
   __device__ void advance(int k) { more[k % 2] = walk.next(seg[k % 2]); }

@@ -64,6 +64,7 @@ __host__ __device__ inline int sequence_fault(const CacheDims& c, int q0, int q1
 // balance when the lengths change.  An item that lies in several runs is joined by the combine
 // kernel from fp32 partial sums.
 constexpr int kStep = 128;
+constexpr int kSms = 148;
 // What an item of few rows costs besides its keys (queries in, partial results joined, results
 // out), in steps: empty steps at its end that weigh in the cut and are never walked.  Measured:
 // 4 us an item against 1.7 us a step; without them the blocks that draw many short items finish
@@ -74,10 +75,18 @@ constexpr int kStep = 128;
 constexpr int kItemSteps = 2;
 constexpr int kRowsTile = 16;      // most rows of a tile of the kernels for few rows
 
+// a / b of whole numbers that are not negative; 64-bit division costs several times the 32-bit
+// one and is needed for huge batches only.
+__host__ __device__ inline long long quotient(long long a, long long b) {
+  if ((((unsigned long long)a | (unsigned long long)b) >> 32) == 0)
+    return (long long)((unsigned)a / (unsigned)b);
+  return a / b;
+}
+
 // sum of floor(a t / m) over t = 0..k, a in {1, 2}
 __host__ __device__ inline long long floor_sum(long long k, int a, long long m) {
   if (a == 2 && m % 2 == 0) a = 1, m /= 2;
-  const long long q = k / m, r = k - q * m;
+  const long long q = quotient(k, m), r = k - q * m;
   if (a == 1) return m * (q * (q - 1) / 2) + q * (r + 1);
   if (m == 1) return k * (k + 1);
   const long long half = (m + 1) / 2;  // the first t of a period with 2 t >= m
@@ -96,7 +105,7 @@ struct SeqWork {
   long long total;    // and of all heads
 
   __host__ __device__ int tile_steps(int t) const {
-    return rising ? steps + (int)((long long)a * (t + 1) / m) + 1 : steps;
+    return rising ? steps + (int)quotient((long long)a * (t + 1), m) + 1 : steps;
   }
   // steps of the tiles before t
   __host__ __device__ long long steps_before(int t) const {
@@ -122,7 +131,7 @@ __host__ __device__ inline SeqWork seq_work(const CacheDims& c, int q0, int q1, 
   const long long rows = (long long)(q1 - q0) * w.G;
   if (rows <= min_rows || rows > max_rows) return w;
   w.qn = q1 - q0;
-  w.tiles = (int)((rows + R - 1) / R);
+  w.tiles = (int)quotient(rows + R - 1, R);
   const int all = (L + kStep - 1) / kStep;
   if (c.causal && c.window > 0) {
     // 15 keys of alignment, the first row's window, the tile's further tokens
@@ -148,15 +157,27 @@ __host__ __device__ inline SeqWork seq_work(const CacheDims& c, int q0, int q1, 
   return w;
 }
 
-// Steps per block: all of them dealt evenly to at most `blocks` blocks, at least min_steps each.
+// Steps per block: all of them dealt evenly to at most `blocks` blocks, at least min_steps each
+// unless there is not even one per SM.
 __host__ __device__ inline long long steps_per_block(long long total, int blocks, int min_steps) {
-  const long long per = (total + blocks - 1) / blocks;
+  const long long per = quotient(total + blocks - 1, blocks);
+  if (total < kSms && total <= blocks) return 1;
   return per < min_steps ? min_steps : per;
+}
+
+// Items of at most this many steps are not split: a run's end that falls inside one moves to the
+// nearer end of the item.  Splitting saves less than the joining costs where an item is a small
+// part of a run (which then gets that much longer or shorter), or short in itself.
+constexpr int kWholeSteps = 4;
+__host__ __device__ inline long long whole_steps(long long per, int tile) {
+  const long long share = per / 8;
+  return tile <= kRowsTile && share < kWholeSteps ? kWholeSteps : share;
 }
 
 // A block's run of steps and where it begins.
 struct Run {
-  long long begin, end, per;  // steps [begin, end) of the launch's total
+  long long begin, end, per;  // steps [begin, end) of the launch's total, before whole items
+  long long whole;            // items of at most so many steps are not split
   int b;                      // the sequence of `begin`
   long long base;             // the total's number of that sequence's first step
 };
@@ -174,23 +195,24 @@ struct Segment {
 // Walks the segments of a run in order; next() is uniform over the block.
 template <typename F>
 struct Walk {
-  long long at, end, per;
+  long long at, end, per, whole;
   long long item;        // the total's number of the current item's first step
   int b, h, tile, n, B;  // the current item, its steps; sequences
+  int heads;             // kv heads
   SeqWork w;
   F work;                // sequence number -> SeqWork
 
-  __host__ __device__ Walk(const F& f, const Run& r, int sequences)
-      : at(r.begin), end(r.end), per(r.per), item(r.base), b(r.b), h(0), tile(0), n(0),
-        B(sequences), work(f) {
+  __host__ __device__ Walk(const F& f, const Run& r, int sequences, int kv_heads)
+      : at(r.begin), end(r.end), per(r.per), whole(r.whole), item(r.base), b(r.b), h(0), tile(0),
+        n(0), B(sequences), heads(kv_heads), work(f) {
     if (at >= end) return;
     w = work(b);
     const long long rel = at - r.base;
-    h = (int)(rel / w.per_head);
+    h = (int)quotient(rel, w.per_head);
     const long long x = rel - h * w.per_head;
     int lo = 0, hi = w.tiles;  // the last tile with steps_before <= x
     if (!w.rising) {
-      lo = (int)(x / w.steps);
+      lo = (int)quotient(x, w.steps);
     } else {
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
@@ -201,6 +223,11 @@ struct Walk {
     tile = lo;
     n = w.tile_steps(tile);
     item = r.base + h * w.per_head + w.steps_before(tile);
+    if (n <= whole) at = nearer(at);
+  }
+  // x inside the current item -> the item's begin or end
+  __host__ __device__ long long nearer(long long x) const {
+    return 2 * (x - item) < n ? item : item + n;
   }
   __host__ __device__ bool next(Segment& s) {
     if (at >= end) return false;
@@ -208,7 +235,7 @@ struct Walk {
       item += n;
       if (++tile >= w.tiles) {
         tile = 0;
-        if (++h >= w.total / (w.per_head > 0 ? w.per_head : 1)) {
+        if (++h >= heads) {
           h = 0;
           do {
             if (++b >= B) return false;
@@ -218,14 +245,19 @@ struct Walk {
       }
       n = w.tile_steps(tile);
     }
+    const long long stop = n <= whole && end < item + n ? nearer(end) : end;
+    if (at >= stop) {  // the item is the next block's
+      at = end;
+      return false;
+    }
     s.b = b, s.h = h, s.tile = tile;
     s.s0 = (int)(at - item);
-    const long long left = end - at;
+    const long long left = stop - at;
     s.s1 = left < n - s.s0 ? s.s0 + (int)left : n;
     s.key0 = w.tile_first(tile);
     s.first = s.s0 == 0;
     s.last = s.s1 == n;
-    s.followers = s.first && !s.last ? (int)((item + n - 1) / per - at / per) : 0;
+    s.followers = s.first && !s.last ? (int)(quotient(item + n - 1, per) - quotient(at, per)) : 0;
     s.w = w;
     at += s.s1 - s.s0;
     return true;
@@ -258,7 +290,6 @@ __host__ __device__ inline KeyRange row_keys(const CacheDims& c, const SeqWork& 
 // tile.  Partial 2c is block c's first item when the item
 // began in an earlier block, 2c + 1 its last item when the item goes on in later blocks.
 constexpr size_t kCacheErrBytes = 1024;
-constexpr int kSms = 148;
 constexpr int kRowsBlocks = 4 * kSms;  // largest launch of the kernels for a few rows
 constexpr int kChunkBlocks = kSms;  // launch of the chunk kernel: 1 per SM
 constexpr int kChunkTile = 256;    // rows of its tiles

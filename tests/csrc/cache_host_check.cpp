@@ -38,11 +38,12 @@ static int check_cut(const ra::CacheDims& c, const Batch& t, int blocks, int til
   for (int blk = 0; blk < blocks; ++blk) {
     ra::Run r{};
     r.per = per;
+    r.whole = ra::whole_steps(per, tile);
     r.begin = blk * per < total ? blk * per : total;
     r.end = r.begin + per < total ? r.begin + per : total;
     for (int b = 0; b < c.B; ++b)
       if (r.begin >= base[b] && r.begin < base[b] + work(b).total) r.b = b, r.base = base[b];
-    ra::Walk<decltype(work)> walk(work, r, c.B);
+    ra::Walk<decltype(work)> walk(work, r, c.B, c.Hkv);
     ra::Segment s;
     int segments = 0, split_here = 0;
     while (walk.next(s)) {
@@ -52,6 +53,7 @@ static int check_cut(const ra::CacheDims& c, const Batch& t, int blocks, int til
           s.s0 >= s.s1 || s.s1 > n)
         return fail("segment range", blk, s.b, s.s0);
       const long long item = base[s.b] + s.h * w.per_head + w.steps_before(s.tile);
+      if (n <= r.whole && (s.s0 != 0 || s.s1 != n)) return fail("short item split", blk, s.b, n);
       if (w.steps_before(s.tile + 1) - w.steps_before(s.tile) != n)
         return fail("steps_before", s.b, s.tile, n);
       // the tile's steps hold every key that one of its rows sees
