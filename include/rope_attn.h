@@ -306,7 +306,7 @@ ra_status rope_attn_rotary_bwd(const ra_rotary* r, int64_t B, int64_t n, int32_t
 typedef struct {
     int64_t B, T;             /* sequences 1..65536; rows of q, k, v, o, lse, 0 <= T <= 2^30 */
     int64_t Hq, Hkv;          /* Hq a multiple of Hkv; Hkv <= 1024, Hq <= 4096,
-                                 T Hq d <= 2^38                                             */
+                                 T Hq d <= 2^36                                             */
     int64_t d;                /* 64 or 128                                                   */
     int64_t pages, page_size; /* 1..2^30; multiple of 16, 16..4096                           */
     int64_t max_pages;        /* width of table; max_pages page_size <= 2^30                 */
@@ -341,11 +341,19 @@ ra_status rope_attn_cache_read(const ra_cache* p, const void* cache, const int32
                                const ra_rows* v, void* ws, size_t ws_bytes, void* stream);
 
 /* o = softmax(scale q K^T + mask) V over the cache, lse = log-sum-exp of each row (natural
- * log).  q [T, Hq, d] rows (already rotated), o dense [T, Hq, d], lse dense fp32 [T, Hq];
- * q head h reads kv head h / (Hq / Hkv).  A row that sees no key gives o = 0, lse = -inf.
- * bf16: tensor cores (mma.sync for a few rows, tcgen05 for chunks); the codes enter the score
- * products exactly, V as fp16 lo + step * code and P as fp16, everything summed in fp32.
- * fp32: CUDA cores, fp32 throughout.  Deterministic: no atomics, fixed order. */
+ * log).  q [T, Hq, d] rows (already rotated), o dense [T, Hq, d] (16-byte aligned), lse dense
+ * fp32 [T, Hq]; q head h reads kv head h / (Hq / Hkv).  A row that sees no key gives o = 0,
+ * lse = -inf.  The pairs of cached tokens must be finite, as appending writes them (what lies
+ * behind kv_len may be anything).  Deterministic: no atomics, fixed order; a sequence's result
+ * does not depend on the others' contents, only (by rounding) on how the lengths cut the work.
+ * Which kernel takes a sequence goes by its own rows (tokens x Hq / Hkv):
+ *   bf16, up to 64 rows: mma.sync on the codes; scores exact to fp32 sums, weights times step
+ *     rounded to fp16.
+ *   bf16, more: tcgen05; K as exact fp16 products (step (code - 8) rounded to fp16 where a row
+ *     sees 4096 keys or more), V rounded to fp16, weights fp16.
+ *   In both q enters as fp16: entries, and in the second kernel sums of 64 channels, beyond
+ *     65504 are clamped and reported as RA_ERR_RANGE.
+ *   fp32: CUDA cores, fp32 throughout. */
 ra_status rope_attn_cache_attn(const ra_cache* p, const void* cache, const int32_t* table,
                                const int32_t* indptr, const int32_t* kv_len, const ra_rows* q,
                                void* o, float* lse, void* ws, size_t ws_bytes, void* stream);

@@ -420,11 +420,15 @@ bool aligned_to(const void* p, size_t a) {
   return p && (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
 
+}  // namespace
+
 // [T, H, d] rows for a cache call; written rows must not overlap.
 ra_status check_token_rows(const ra_rows* r, const ra_cache& p, int64_t H, bool written) {
   if (!r || !aligned_to(r->ptr, elem_bytes(p.dtype)) || r->H != H) return RA_ERR_INVALID_ARG;
-  if (r->stride_n < 0 || r->stride_h < 0 || r->stride_n > (int64_t(1) << 40) ||
-      r->stride_h > (int64_t(1) << 40))
+  // no offset beyond 2^45 elements
+  if (r->stride_n < 0 || r->stride_h < 0 ||
+      r->stride_n > (int64_t(1) << 44) / std::max<int64_t>(1, p.T) ||
+      r->stride_h > (int64_t(1) << 44) / H)
     return RA_ERR_INVALID_ARG;
   if (written) {
     const bool n_outer = r->stride_n >= r->stride_h;
@@ -436,6 +440,8 @@ ra_status check_token_rows(const ra_rows* r, const ra_cache& p, int64_t H, bool 
   }
   return RA_OK;
 }
+
+namespace {
 
 int vectors_fit(const ra_rows& r, int32_t dtype) {
   const int64_t V = (int64_t)(16 / elem_bytes(dtype));
@@ -476,7 +482,7 @@ ra_status check_cache(const ra_cache* p) {
       p->pages > (int64_t(1) << 30) || p->page_size > 4096 || p->window > (int64_t(1) << 30) ||
       p->max_q > (int64_t(1) << 30) || p->max_pages > (int64_t(1) << 30) / p->page_size)
     return RA_ERR_UNSUPPORTED;
-  if (p->T * p->Hq > (int64_t(1) << 38) / p->d) return RA_ERR_UNSUPPORTED;
+  if (p->T * p->Hq > (int64_t(1) << 36) / p->d) return RA_ERR_UNSUPPORTED;
   if (p->Hq % p->Hkv) return RA_ERR_INVALID_ARG;
   return RA_OK;
 }

@@ -132,8 +132,10 @@ __global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const __gri
 #pragma unroll
         for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
         const float m_new = fmaxf(m[r], mx);
-        float p = 0.f;
-        if (m_new != -CUDART_INF_F) {
+        float p = isnan(x) ? x : 0.f;  // a NaN query gives a NaN row, also where nothing is finite
+        if (m_new == -CUDART_INF_F) {
+          l[r] += p;
+        } else {
           const float corr = exp2f(m[r] - m_new);
           p = exp2f(x - m_new);
           l[r] = l[r] * corr + p;
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const __gri
       if (whole) {
         const long long row = row0 + r;
         const long long at = (s.w.q0 + row / G) * c.Hq + (long long)s.h * G + row % G;
-        static_cast<float*>(a.o)[at * D + ch] = wl > 0.f ? sum / wl : 0.f;
+        static_cast<float*>(a.o)[at * D + ch] = wl == 0.f ? 0.f : sum / wl;
         if (ch == 0) a.lse[at] = (mx + log2f(wl)) * 0.6931471805599453f;
       } else {
         a.acc[(slot * a.tile + r) * D + ch] = sum;
@@ -257,7 +259,7 @@ __global__ void __launch_bounds__(kCombineThreads)
   auto write = [&](int r, int ch, const float* x, int n, float mx, float l) {
     const long long row = row0 + r, token = row / G;
     const long long at = (q0 + token) * c.Hq + (long long)d.h * G + (row - token * G);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
 #pragma unroll
     for (int e = 0; e < DL; ++e) {
       if (e >= n) break;
@@ -317,16 +319,15 @@ __global__ void __launch_bounds__(kCombineThreads)
     float acc[DL], l = 0.f;
 #pragma unroll
     for (int e = 0; e < DL; ++e) acc[e] = 0.f;
-    if (mx != -CUDART_INF_F) {
 #pragma unroll 8
-      for (int k = warp; k < parts; k += kCombineWarps) {
-        const long long at = slot_of(k) * a.tile + r;
-        const float f = exp2f(a.ml[at * 2] - mx);
-        l = fmaf(f, a.ml[at * 2 + 1], l);
-        const float* src = a.acc + at * D + lane * DL;
+    for (int k = warp; k < parts; k += kCombineWarps) {
+      const long long at = slot_of(k) * a.tile + r;
+      const float m = a.ml[at * 2];
+      const float f = m == -CUDART_INF_F ? 0.f : exp2f(m - mx);
+      l = fmaf(f, a.ml[at * 2 + 1], l);
+      const float* src = a.acc + at * D + lane * DL;
 #pragma unroll
-        for (int e = 0; e < DL; ++e) acc[e] = fmaf(f, src[e], acc[e]);
-      }
+      for (int e = 0; e < DL; ++e) acc[e] = fmaf(f, src[e], acc[e]);
     }
 #pragma unroll
     for (int e = 0; e < DL; ++e) red[warp][lane * DL + e] = acc[e];
@@ -393,11 +394,8 @@ ra_status rope_attn_cache_attn(const ra_cache* p, const void* cache, const int32
   ra_status st = check_cache_call(p, cache, table, indptr, kv_len, ws, ws_bytes);
   if (st != RA_OK) return st;
   if (p->T == 0) return RA_OK;
-  const size_t elem = elem_bytes(p->dtype);
-  const int64_t V = (int64_t)(16 / elem);
-  if (!q || !q->ptr || (uintptr_t)q->ptr % elem || q->H != p->Hq || q->stride_n < 0 ||
-      q->stride_h < 0 || q->stride_n > (int64_t(1) << 40) || q->stride_h > (int64_t(1) << 40))
-    return RA_ERR_INVALID_ARG;
+  const int64_t V = (int64_t)(16 / elem_bytes(p->dtype));
+  if ((st = check_token_rows(q, *p, p->Hq, false)) != RA_OK) return st;
   if (!o || (uintptr_t)o % 16 || !lse || (uintptr_t)lse % 4) return RA_ERR_INVALID_ARG;
   AttnArgs a{};
   a.c = cache_dims(*p);

@@ -55,7 +55,9 @@ inline cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, unsigned b
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) cudaGetLastError();  // reported by the status, not left behind
+  return e;
 }
 #ifdef __CUDACC__
 __device__ __forceinline__ void grid_wait() {

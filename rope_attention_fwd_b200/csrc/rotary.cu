@@ -240,8 +240,9 @@ ra_status check_rows(const ra_rows* r, const ra_rotary& s, int64_t B, int64_t n,
                      bool written) {
   if (!r || !r->ptr || !aligned_to(r->ptr, elem_bytes(dtype))) return RA_ERR_INVALID_ARG;
   if (r->H < 1 || r->H > kMaxHeads) return RA_ERR_INVALID_ARG;
-  for (int64_t st : {r->stride_b, r->stride_h, r->stride_n})
-    if (st < 0 || st > (int64_t(1) << 40)) return RA_ERR_INVALID_ARG;
+  const int64_t ext[3] = {B, r->H, n}, st[3] = {r->stride_b, r->stride_h, r->stride_n};
+  for (int i = 0; i < 3; ++i)  // no offset beyond 2^46 elements
+    if (st[i] < 0 || st[i] > (int64_t(1) << 44) / ext[i]) return RA_ERR_INVALID_ARG;
   if (written && !rows_distinct(*r, B, n, s.d)) return RA_ERR_INVALID_ARG;
   return RA_OK;
 }

@@ -306,6 +306,7 @@ struct CacheWs {
 #ifdef __CUDACC__
 ra_status check_cache(const ra_cache* p);
 CacheDims cache_dims(const ra_cache& p);
+ra_status check_token_rows(const ra_rows* r, const ra_cache& p, int64_t H, bool written);
 ra_status check_cache_call(const ra_cache* p, const void* cache, const int32_t* table,
                            const int32_t* indptr, const int32_t* kv_len, void* ws,
                            size_t ws_bytes);

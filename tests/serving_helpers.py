@@ -126,7 +126,7 @@ class Batch:
             worst = max(worst, float((err / tol).max()) if err.size else 0.0)
             empty = np.isinf(wl)
             assert (np.isneginf(lse[at]) == empty).all() and (o[at][empty] == 0).all(), (label, b)
-            el = abs(lse[at] - wl)[~empty]
+            el = abs(lse[at][~empty] - wl[~empty])
             tl = (ds[..., 0] + 2.0 ** -19 + 2 * U * abs(np.where(empty, 0, wl)))[~empty]
             if bf:
                 tl = tl + L * 2.0 ** -25

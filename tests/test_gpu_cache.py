@@ -113,6 +113,60 @@ def test_host_tensors_are_refused():
         rb.rope_attn_cache_attn(*b.head, b.c["q"].cpu(), ws=b.c["ws"])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_nan_queries_stay_in_their_rows(dtype):
+    b = Batch([(1, 40), (4, 700), (80, 90)], 4, 2, 64, 16, dtype, seed=21).device()
+    o, lse = (t.clone() for t in b.attn())
+    rows = [(0, 1), (2, 3), (30, 0)]
+    for t, h in rows:
+        b.c["q"][t, h, 5] = float("nan")
+    o2, lse2 = b.attn()
+    hit = torch.zeros((b.T, 4), dtype=torch.bool, device="cuda")
+    for t, h in rows:
+        hit[t, h] = True
+    assert o2[hit].isnan().all() and lse2[hit].isnan().all()
+    assert torch.equal(o2[~hit], o[~hit]) and torch.equal(lse2[~hit], lse[~hit])
+    assert rb.STATUS[b.status()[0]] == ("RA_ERR_RANGE" if dtype == "bf16" else "RA_OK")
+
+
+def test_large_queries_are_clamped_and_reported():
+    for n, L in ((1, 30), (80, 90)):
+        b = Batch([(n, L)], 4, 2, 64, 16, "bf16", seed=22).device()
+        b.attn()
+        assert b.status()[0] == 0
+        b.c["q"][0, 0, 0] = 7e4
+        o, lse = b.attn()
+        assert rb.STATUS[b.status()[0]] == "RA_ERR_RANGE"
+        assert o.isfinite().all() and lse.isfinite().all()
+
+
+def test_calls_on_two_streams_with_a_workspace_each():
+    bs = [Batch([(1, 900), (2, 300), (90, 100)], 8, 2, 128, 16, "bf16", seed=30 + i).device()
+          for i in range(2)]
+    want = [[t.clone() for t in b.attn()] for b in bs]
+    streams = [torch.cuda.Stream() for _ in bs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(10):
+        for i, (b, s) in enumerate(zip(bs, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(b.attn())
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for o, lse in g:
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+
+
+def test_a_sequence_does_not_depend_on_its_neighbours_contents():
+    b = Batch([(1, 300), (3, 500), (70, 90), (1, 40)], 8, 2, 64, 16, "bf16", seed=33).device()
+    o, lse = (t.clone() for t in b.attn())
+    b.c["q"][1:4] *= 3        # the second sequence's queries
+    o2, lse2 = b.attn()
+    keep = [0] + list(range(4, b.T))
+    assert torch.equal(o[keep], o2[keep]) and torch.equal(lse[keep], lse2[keep])
+
+
 def test_scale_is_taken():
     b = Batch([(1, 100), (70, 90)], 4, 2, 64, 16, "bf16", scale=0.05).device()
     b.check(*b.attn())
