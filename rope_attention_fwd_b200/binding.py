@@ -383,8 +383,29 @@ def rope_attn_alpha_adam(alpha, dalpha, m1, m2, step, lr, beta1=0.9, beta2=0.999
 
 
 # ---------------------------------------------------------------- rotation, paged cache
-# A decode step makes several of these calls per layer on little work, so the checks go by the
-# cheapest attributes (get_device, dtype, shape) and build nothing unless they fail.
+# A decode step makes several of these calls per layer on little work.  In their plain form
+# (outputs to be allocated, a workspace given, everything in order and on the current device) the
+# extension _marshal (csrc/marshal.cpp) makes the same checks and the same C call; it returns
+# None for anything else, which then goes the general way below.
+def _load_marshal():
+    try:
+        from . import _marshal
+    except ImportError:      # not built: the general way serves every call
+        return None
+    return _marshal
+
+
+_fast = _load_marshal()
+_address = ctypes.addressof
+
+
+def _done(fn, out):
+    """The outputs of a _marshal call, or its status raised."""
+    if out.__class__ is int:
+        raise RopeAttnError(fn, out)
+    return out
+
+
 def _serving_device(fn, t):
     """The index of t's CUDA device (the calls below take device memory only)."""
     if not t.is_cuda:
@@ -457,6 +478,10 @@ def rope_attn_rotary_freqs(spec, alpha=None, freqs=None, device=None):
     alpha (fp32 [rot_dim/2]; None: zeros, on `device`).  Kept by the caller for the calls below;
     computed anew whenever alpha changes."""
     fn = "rope_attn_rotary_freqs"
+    if _fast is not None and freqs is None and alpha is not None:
+        out = _fast.rotary_freqs(_address(spec), alpha)
+        if out is not None:
+            return _done(fn, out)
     half = spec.rot_dim // 2
     if freqs is None:
         freqs = alpha.new_empty(half, dtype=torch.float64) if alpha is not None else \
@@ -493,6 +518,10 @@ def rope_attn_rotary(spec, freqs, q, k=None, pos=None, q_out=None, k_out=None):
     """(q~, k~): q [B, Hq, n, d] and k [B, Hk, n, d] (any strides, channels contiguous; k may be
     None) rotated at positions pos (int32 [B, n]; None: 0..n-1).  q_out may be q, k_out k."""
     fn = "rope_attn_rotary"
+    if _fast is not None and q_out is None and k_out is None:
+        out = _fast.rotary(_address(spec), freqs, q, k, pos)
+        if out is not None:
+            return _done(fn, out)
     dev, head = _rotary_args(fn, spec, freqs, q, pos)
     dt, shape = q.dtype, q.shape
     q_out = torch.empty_like(q) if q_out is None else q_out
@@ -517,6 +546,11 @@ def rope_attn_rotary_bwd(spec, freqs, dq_rot, dk_rot=None, q=None, k=None, pos=N
     """(dq, dk, dalpha) from the gradients dq_rot, dk_rot of the rotated tensors.  q and k (the
     forward's inputs) are needed for dalpha only; frozen_alpha: None is returned in its place."""
     fn = "rope_attn_rotary_bwd"
+    if _fast is not None and not frozen_alpha and dq is None and dk is None and dalpha is None \
+            and ws is None:
+        out = _fast.rotary_bwd(_address(spec), freqs, dq_rot, dk_rot, q, k, pos)
+        if out is not None:
+            return _done(fn, out)
     dev, head = _rotary_args(fn, spec, freqs, dq_rot, pos)
     dt, q_shape, k_shape = dq_rot.dtype, dq_rot.shape, None
     dq = torch.empty_like(dq_rot) if dq is None else dq
@@ -619,6 +653,11 @@ def rope_attn_cache_append(plan, cache, table, indptr, kv_len, spec, freqs, k, v
     counts the appended tokens already.  Device-side faults (a bad page, length or offset, a
     value beyond the cache's range) stay in ws for rope_attn_device_status."""
     fn = "rope_attn_cache_append"
+    if _fast is not None and q_out is None:
+        out = _fast.cache_append(_address(plan), cache, table, indptr, kv_len, _address(spec),
+                                 freqs, k, v, q, ws)
+        if out is not None:
+            return _done(fn, out)[0]
     dev, head, tail, dt = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)
     kv = (plan.T, plan.Hkv, plan.d)
     f = _vector(fn, "freqs", freqs, dev, torch.float64, (spec.rot_dim // 2,))
@@ -636,6 +675,10 @@ def rope_attn_cache_read(plan, cache, table, indptr, kv_len, k=None, v=None, ws=
     """(k, v) [T, Hkv, d]: the cached rows of the batch's tokens as the values they stand for
     (for a whole cache, give indptr the running sum of kv_len)."""
     fn = "rope_attn_cache_read"
+    if _fast is not None and k is None and v is None:
+        out = _fast.cache_read(_address(plan), cache, table, indptr, kv_len, ws)
+        if out is not None:
+            return _done(fn, out)
     dev, head, tail, dt = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)
     kv = (plan.T, plan.Hkv, plan.d)
     k = cache.new_empty(kv, dtype=dt) if k is None else k
@@ -650,6 +693,10 @@ def rope_attn_cache_attn(plan, cache, table, indptr, kv_len, q, o=None, lse=None
     """(o [T, Hq, d], lse fp32 [T, Hq]): attention of the rotated queries q [T, Hq, d] over the
     cache.  Rows that belong to no sequence are left as they were."""
     fn = "rope_attn_cache_attn"
+    if _fast is not None and o is None and lse is None:
+        out = _fast.cache_attn(_address(plan), cache, table, indptr, kv_len, q, ws)
+        if out is not None:
+            return _done(fn, out)
     dev, head, tail, dt = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)
     T, Hq = plan.T, plan.Hq
     qs = (T, Hq, plan.d)

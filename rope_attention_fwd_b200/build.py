@@ -4,7 +4,9 @@
 
 Every ``csrc/*.cu`` is compiled to an object under ``_build/`` (in parallel,
 only when its sources changed) and linked into
-``rope_attention_fwd_b200/librope_attn.so`` next to this file.
+``rope_attention_fwd_b200/librope_attn.so`` next to this file; ``csrc/marshal.cpp``
+becomes the Python extension ``_marshal.so`` beside it (host code only, against
+torch's headers and librope_attn.so).
 """
 import argparse
 import concurrent.futures as cf
@@ -12,12 +14,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "librope_attn.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC,-O2", "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
@@ -46,6 +50,27 @@ def _compile(src, verbose):
     return obj, r.stderr
 
 
+def _build_marshal():
+    """The Python extension that marshals the serving calls."""
+    src = os.path.join(CSRC, "marshal.cpp")
+    if not _stale(MARSHAL, [src, os.path.join(ROOT, "include", "rope_attn.h"),
+                            os.path.abspath(__file__)]):
+        return
+    import torch
+    from torch.utils import cpp_extension as ext
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", src, "-o", MARSHAL,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + os.path.join(ROOT, "include"), "-I" + sysconfig.get_paths()["include"],
+           "-I" + os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    cmd += ["-I" + p for p in ext.include_paths()]
+    cmd += ["-L" + libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-L" + PKG,
+            "-lrope_attn", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+
+
 def build(force=False, verbose=False):
     """Compile (if needed) and return the path of librope_attn.so."""
     os.makedirs(BUILD, exist_ok=True)
@@ -65,6 +90,9 @@ def build(force=False, verbose=False):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    if force and os.path.exists(MARSHAL):
+        os.remove(MARSHAL)
+    _build_marshal()
     return LIB
 
 

@@ -1,0 +1,312 @@
+// marshal.cpp -- the serving calls' argument marshalling in C++ (Python extension _marshal).
+//
+// A decode step makes a handful of these calls per layer on a few microseconds of GPU work each;
+// checking and converting their tensors in Python took 9 of the 13 us of a call.  Each function
+// here takes the call in its plain form (outputs to be allocated, every tensor of the right
+// type, shape and device, the device current), makes the same checks as binding.py, allocates
+// the outputs and calls the C ABI.  It returns the outputs, the status as an int if that is not
+// RA_OK, or None if anything is not in the plain form: binding.py then goes its general way, with
+// its messages.  No compute happens here.
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "rope_attn.h"
+
+namespace {
+
+using at::ScalarType;
+using at::Tensor;
+
+PyObject* none() { Py_RETURN_NONE; }
+
+// The tensor of argument i, or null if it is none.
+const Tensor* tensor(PyObject* const* args, int i) {
+  return THPVariable_Check(args[i]) ? &THPVariable_Unpack(args[i]) : nullptr;
+}
+
+template <typename T>
+const T* address(PyObject* o) {
+  return static_cast<const T*>(PyLong_AsVoidPtr(o));
+}
+
+// The current CUDA device, which every tensor has to be on.
+struct Here {
+  int dev;
+  explicit Here(const Tensor* t)
+      : dev(t && t->is_cuda() && t->get_device() == c10::cuda::current_device() ? t->get_device()
+                                                                               : -1) {}
+  bool ok() const { return dev >= 0; }
+  void* stream() const { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
+  bool vector(const Tensor* t, ScalarType type, at::IntArrayRef shape) const {
+    return t && t->is_cuda() && t->get_device() == dev && t->scalar_type() == type &&
+           t->sizes() == shape && t->is_contiguous();
+  }
+  // [B, H, n, d] or [T, H, d] rows of heads with contiguous channels
+  bool rows(const Tensor* t, ScalarType type, at::IntArrayRef shape, ra_rows& r) const {
+    if (!t || !t->is_cuda() || t->get_device() != dev || t->scalar_type() != type ||
+        t->sizes() != shape)
+      return false;
+    const auto st = t->strides();
+    const size_t n = shape.size();
+    if (st[n - 1] != 1) return false;
+    r.ptr = t->data_ptr();
+    r.H = shape[1];
+    if (n == 4) r.stride_b = st[0], r.stride_h = st[1], r.stride_n = st[2];
+    else r.stride_b = 0, r.stride_h = st[1], r.stride_n = st[0];
+    return true;
+  }
+};
+
+bool type_of(int32_t dtype, ScalarType& t) {
+  t = dtype == RA_BF16 ? ScalarType::BFloat16 : ScalarType::Float;
+  return dtype == RA_BF16 || dtype == RA_F32;
+}
+
+PyObject* wrap(const Tensor& t) { return THPVariable_Wrap(t); }
+PyObject* status(ra_status s) { return PyLong_FromLong((long)s); }
+
+// An exception of the allocator (out of memory) becomes Python's; nothing else throws here.
+template <typename F>
+PyObject* guarded(F f) {
+  try {
+    return f();
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
+// (spec address, alpha)
+PyObject* rotary_freqs(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 2) return none();
+    const auto* spec = address<ra_rotary>(a[0]);
+    const Tensor* alpha = tensor(a, 1);
+    const Here here(alpha);
+    const int64_t half = spec->rot_dim / 2;
+    if (!here.ok() || !here.vector(alpha, ScalarType::Float, {half})) return none();
+    Tensor f = at::empty({half}, alpha->options().dtype(ScalarType::Double));
+    const ra_status s = rope_attn_rotary_freqs(spec, alpha->data_ptr<float>(),
+                                               f.data_ptr<double>(), here.stream());
+    return s == RA_OK ? wrap(f) : status(s);
+  });
+}
+
+// What both directions of the rotation share: dtype, sizes, frequencies, positions.
+struct RotaryCall {
+  const ra_rotary* spec = nullptr;
+  int64_t B = 0, n = 0;
+  int32_t dtype = 0;
+  const double* freqs = nullptr;
+  const int32_t* pos = nullptr;
+  bool take(const Here& here, PyObject* sp, const Tensor* f, const Tensor* x, PyObject* p,
+            const Tensor* pt) {
+    spec = address<ra_rotary>(sp);
+    if (!x || x->dim() != 4 || x->size(3) != spec->d) return false;
+    if (x->scalar_type() != ScalarType::BFloat16 && x->scalar_type() != ScalarType::Float)
+      return false;
+    dtype = x->scalar_type() == ScalarType::BFloat16 ? RA_BF16 : RA_F32;
+    B = x->size(0), n = x->size(2);
+    if (!here.vector(f, ScalarType::Double, {spec->rot_dim / 2})) return false;
+    freqs = f->data_ptr<double>();
+    if (p != Py_None) {
+      if (!here.vector(pt, ScalarType::Int, {B, n})) return false;
+      pos = pt->data_ptr<int32_t>();
+    }
+    return true;
+  }
+};
+
+bool same_tokens(const Tensor& a, const Tensor& b) {
+  return a.dim() == 4 && a.size(0) == b.size(0) && a.size(2) == b.size(2) &&
+         a.size(3) == b.size(3);
+}
+
+// (spec address, freqs, q, k or None, pos or None)
+PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 5) return none();
+    const Tensor *f = tensor(a, 1), *q = tensor(a, 2), *k = tensor(a, 3);
+    const Here here(q);
+    RotaryCall c;
+    if (!here.ok() || !c.take(here, a[0], f, q, a[4], tensor(a, 4))) return none();
+    const ScalarType type = q->scalar_type();
+    ra_rows qi, qo, ki, ko;
+    if (!here.rows(q, type, q->sizes(), qi)) return none();
+    if (a[3] != Py_None && (!k || !same_tokens(*k, *q) || !here.rows(k, type, k->sizes(), ki)))
+      return none();
+    Tensor q_out = at::empty_like(*q), k_out;
+    if (!here.rows(&q_out, type, q->sizes(), qo)) return none();
+    if (k) {
+      k_out = at::empty_like(*k);
+      if (!here.rows(&k_out, type, k->sizes(), ko)) return none();
+    }
+    const ra_status s = rope_attn_rotary(c.spec, c.B, c.n, c.dtype, c.freqs, c.pos, &qi, &qo,
+                                         k ? &ki : nullptr, k ? &ko : nullptr, here.stream());
+    if (s != RA_OK) return status(s);
+    PyObject* out = PyTuple_New(2);
+    PyTuple_SET_ITEM(out, 0, wrap(q_out));
+    PyTuple_SET_ITEM(out, 1, k ? wrap(k_out) : none());
+    return out;
+  });
+}
+
+// (spec address, freqs, dq_rot, dk_rot or None, q, k or None, pos or None): with dalpha
+PyObject* rotary_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 7) return none();
+    const Tensor *f = tensor(a, 1), *gq = tensor(a, 2), *gk = tensor(a, 3), *q = tensor(a, 4),
+                 *k = tensor(a, 5);
+    const Here here(gq);
+    RotaryCall c;
+    if (!here.ok() || !c.take(here, a[0], f, gq, a[6], tensor(a, 6))) return none();
+    const ScalarType type = gq->scalar_type();
+    ra_rows gqi, gqo, qi, gki, gko, ki;
+    if (!here.rows(gq, type, gq->sizes(), gqi) || !here.rows(q, type, gq->sizes(), qi))
+      return none();
+    if ((a[3] != Py_None) != (a[5] != Py_None)) return none();
+    if (a[3] != Py_None &&
+        (!gk || !same_tokens(*gk, *gq) || !here.rows(gk, type, gk->sizes(), gki) ||
+         !here.rows(k, type, gk->sizes(), ki)))
+      return none();
+    const size_t bytes = rope_attn_rotary_workspace_bytes(c.spec);
+    Tensor dq = at::empty_like(*gq), dk;
+    if (!here.rows(&dq, type, gq->sizes(), gqo)) return none();
+    if (gk) {
+      dk = at::empty_like(*gk);
+      if (!here.rows(&dk, type, gk->sizes(), gko)) return none();
+    }
+    Tensor da = at::empty({c.spec->rot_dim / 2}, gq->options().dtype(ScalarType::Float));
+    Tensor ws = at::empty({(int64_t)bytes}, gq->options().dtype(ScalarType::Byte));
+    const ra_status s = rope_attn_rotary_bwd(
+        c.spec, c.B, c.n, c.dtype, c.freqs, c.pos, &gqi, &gqo, gk ? &gki : nullptr,
+        gk ? &gko : nullptr, &qi, gk ? &ki : nullptr, da.data_ptr<float>(), ws.data_ptr(), bytes,
+        here.stream());
+    if (s != RA_OK) return status(s);
+    PyObject* out = PyTuple_New(3);
+    PyTuple_SET_ITEM(out, 0, wrap(dq));
+    PyTuple_SET_ITEM(out, 1, gk ? wrap(dk) : none());
+    PyTuple_SET_ITEM(out, 2, wrap(da));
+    return out;
+  });
+}
+
+// The leading arguments of a cache call: plan address, cache, table, indptr, kv_len; and ws.
+struct CacheCall {
+  const ra_cache* p = nullptr;
+  ScalarType type = ScalarType::Float;
+  void *cache = nullptr, *ws = nullptr;
+  const int32_t *table = nullptr, *indptr = nullptr, *kv_len = nullptr;
+  size_t ws_bytes = 0;
+  bool take(const Here& here, PyObject* const* a, const Tensor* c, const Tensor* w) {
+    p = address<ra_cache>(a[0]);
+    const size_t want = rope_attn_cache_bytes(p);
+    if (!want || !type_of(p->dtype, type)) return false;
+    const Tensor *t = tensor(a, 2), *i = tensor(a, 3), *l = tensor(a, 4);
+    if (c->scalar_type() != ScalarType::Byte || !c->is_contiguous() ||
+        (size_t)c->numel() != want || !here.vector(t, ScalarType::Int, {p->B, p->max_pages}) ||
+        !here.vector(i, ScalarType::Int, {p->B + 1}) ||
+        !here.vector(l, ScalarType::Int, {p->B}) || !w ||
+        !here.vector(w, ScalarType::Byte, {w->numel()}))
+      return false;
+    cache = c->data_ptr(), ws = w->data_ptr(), ws_bytes = (size_t)w->numel();
+    table = t->data_ptr<int32_t>(), indptr = i->data_ptr<int32_t>();
+    kv_len = l->data_ptr<int32_t>();
+    return true;
+  }
+};
+
+// (plan, cache, table, indptr, kv_len, spec, freqs, k, v, q or None, ws)
+PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 11) return none();
+    const Tensor *cache = tensor(a, 1), *f = tensor(a, 6), *k = tensor(a, 7), *v = tensor(a, 8),
+                 *q = tensor(a, 9);
+    const Here here(cache);
+    CacheCall c;
+    if (!here.ok() || !c.take(here, a, cache, tensor(a, 10))) return none();
+    const auto* spec = address<ra_rotary>(a[5]);
+    const ra_cache& p = *c.p;
+    ra_rows kr, vr, qi, qo;
+    if (!here.vector(f, ScalarType::Double, {spec->rot_dim / 2}) ||
+        !here.rows(k, c.type, {p.T, p.Hkv, p.d}, kr) ||
+        !here.rows(v, c.type, {p.T, p.Hkv, p.d}, vr))
+      return none();
+    Tensor q_out;
+    if (a[9] != Py_None) {
+      if (!here.rows(q, c.type, {p.T, p.Hq, p.d}, qi)) return none();
+      q_out = at::empty_like(*q);
+      if (!here.rows(&q_out, c.type, {p.T, p.Hq, p.d}, qo)) return none();
+    }
+    const ra_status s = rope_attn_cache_append(
+        c.p, c.cache, c.table, c.indptr, c.kv_len, spec, f->data_ptr<double>(), &kr, &vr,
+        q ? &qi : nullptr, q ? &qo : nullptr, c.ws, c.ws_bytes, here.stream());
+    if (s != RA_OK) return status(s);
+    PyObject* out = PyTuple_New(1);  // a tuple: None alone means "not here"
+    PyTuple_SET_ITEM(out, 0, q ? wrap(q_out) : none());
+    return out;
+  });
+}
+
+// (plan, cache, table, indptr, kv_len, ws)
+PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 6) return none();
+    const Tensor* cache = tensor(a, 1);
+    const Here here(cache);
+    CacheCall c;
+    if (!here.ok() || !c.take(here, a, cache, tensor(a, 5))) return none();
+    const ra_cache& p = *c.p;
+    Tensor k = at::empty({p.T, p.Hkv, p.d}, cache->options().dtype(c.type));
+    Tensor v = at::empty_like(k);
+    ra_rows kr, vr;
+    if (!here.rows(&k, c.type, k.sizes(), kr) || !here.rows(&v, c.type, v.sizes(), vr))
+      return none();
+    const ra_status s = rope_attn_cache_read(c.p, c.cache, c.table, c.indptr, c.kv_len, &kr, &vr,
+                                             c.ws, c.ws_bytes, here.stream());
+    if (s != RA_OK) return status(s);
+    PyObject* out = PyTuple_New(2);
+    PyTuple_SET_ITEM(out, 0, wrap(k));
+    PyTuple_SET_ITEM(out, 1, wrap(v));
+    return out;
+  });
+}
+
+// (plan, cache, table, indptr, kv_len, q, ws)
+PyObject* cache_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 7) return none();
+    const Tensor *cache = tensor(a, 1), *q = tensor(a, 5);
+    const Here here(cache);
+    CacheCall c;
+    if (!here.ok() || !c.take(here, a, cache, tensor(a, 6))) return none();
+    const ra_cache& p = *c.p;
+    ra_rows qr;
+    if (!here.rows(q, c.type, {p.T, p.Hq, p.d}, qr)) return none();
+    Tensor o = at::empty({p.T, p.Hq, p.d}, q->options());
+    Tensor lse = at::empty({p.T, p.Hq}, q->options().dtype(ScalarType::Float));
+    const ra_status s =
+        rope_attn_cache_attn(c.p, c.cache, c.table, c.indptr, c.kv_len, &qr, o.data_ptr(),
+                             lse.data_ptr<float>(), c.ws, c.ws_bytes, here.stream());
+    if (s != RA_OK) return status(s);
+    PyObject* out = PyTuple_New(2);
+    PyTuple_SET_ITEM(out, 0, wrap(o));
+    PyTuple_SET_ITEM(out, 1, wrap(lse));
+    return out;
+  });
+}
+
+#define RA_METHOD(f) {#f, reinterpret_cast<PyCFunction>(f), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {RA_METHOD(rotary_freqs), RA_METHOD(rotary),     RA_METHOD(rotary_bwd),
+                         RA_METHOD(cache_append), RA_METHOD(cache_read), RA_METHOD(cache_attn),
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
+                      nullptr,               nullptr,    nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__marshal(void) { return PyModule_Create(&module); }

@@ -164,6 +164,26 @@ def test_binding_refuses_host_tensors_and_bad_names():
         rb.rotary_spec(64, scaling="other")
 
 
+def test_marshal_extension_declines_what_is_not_plain():
+    """The C++ marshalling is built, takes no host tensor and no wrong argument: None, which
+    sends the call the general way."""
+    assert rb._fast is not None, "run python -m rope_attention_fwd_b200.build"
+    import ctypes as c
+    s, p = rb.rotary_spec(64), _plan()
+    x = torch.zeros((1, 2, 3, 64))
+    f = torch.zeros(32, dtype=torch.float64)
+    for args in ((c.addressof(s), f, x, None, None), (c.addressof(s), f, None, None, None),
+                 (c.addressof(s), 3, "x", 5, 1.0), ()):
+        assert rb._fast.rotary(*args) is None
+    assert rb._fast.rotary_bwd(c.addressof(s), f, x, None, x, None, None) is None
+    assert rb._fast.rotary_freqs(c.addressof(s), f) is None
+    z = torch.zeros(8, dtype=torch.uint8)
+    assert rb._fast.cache_read(c.addressof(p), z, z, z, z, z) is None
+    assert rb._fast.cache_attn(c.addressof(p), z, None, z, z, z, z) is None
+    assert rb._fast.cache_append(c.addressof(p), z, z, z, z, c.addressof(s), f, z, z, None,
+                                 None) is None
+
+
 class FakeLib:
     def __init__(self):
         self.calls = []
@@ -181,6 +201,7 @@ def fake(monkeypatch):
     f = FakeLib()
     monkeypatch.setattr(rb, "lib", lambda: f)
     monkeypatch.setattr(rb, "_stream", lambda device: ctypes.c_void_p(0))
+    monkeypatch.setattr(rb, "_fast", None)       # the general way (the extension takes CUDA only)
     monkeypatch.setattr(rb, "_raw_stream", lambda index: 0)
     monkeypatch.setattr(rb, "_serving_device", lambda fn, t: t.get_device())   # -1: host memory
     monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)

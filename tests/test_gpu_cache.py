@@ -102,6 +102,41 @@ def test_query_strides(dtype):
     assert torch.equal(o, o2) and torch.equal(lse, l2)
 
 
+def test_both_ways_of_marshalling_agree(monkeypatch):
+    """The extension's and the general way's calls give the same bits, and the same refusals."""
+    b = Batch([(1, 40), (20, 90), (80, 100)], 8, 2, 64, 16, "bf16", seed=40).device()
+    spec = rb.rotary_spec(64, layout="half")
+    alpha = 0.1 * torch.randn(32, device="cuda")
+    kv = torch.randn((b.T, 2, 64), device="cuda").bfloat16()
+    x = torch.randn((2, 3, 50, 64), device="cuda").bfloat16()
+    pos = torch.arange(100, dtype=torch.int32, device="cuda").view(2, 50)
+    results = []
+    for fast in (rb._fast, None):
+        assert fast is not None or results
+        monkeypatch.setattr(rb, "_fast", fast)
+        f = rb.rope_attn_rotary_freqs(spec, alpha)
+        b.c["cache"].copy_(torch.from_numpy(b.cache))
+        r = [f, *rb.rope_attn_rotary(spec, f, x, x[:, :1], pos=pos),
+             *rb.rope_attn_rotary_bwd(spec, f, x, x[:, :2], q=x, k=x[:, 1:], pos=pos),
+             *rb.rope_attn_rotary(spec, f, x)[:1],
+             rb.rope_attn_cache_append(*b.head, spec, f, kv, kv, q=b.c["q"], ws=b.c["ws"])]
+        r += [b.c["cache"].clone(), *rb.rope_attn_cache_read(*b.head, ws=b.c["ws"]), *b.attn()]
+        assert rb.rope_attn_cache_append(*b.head, spec, f, kv, kv, ws=b.c["ws"]) is None
+        results.append(r)
+        with pytest.raises(ValueError):
+            rb.rope_attn_cache_attn(*b.head, b.c["q"].float(), ws=b.c["ws"])
+        with pytest.raises(ValueError):
+            rb.rope_attn_rotary(spec, f, x, x[:, :, :10])
+        with pytest.raises(ValueError):
+            rb.rope_attn_cache_read(b.plan, b.c["cache"][1:], *b.head[2:], ws=b.c["ws"])
+        small = b.c["ws"][:4096]
+        with pytest.raises(rb.RopeAttnError) as e:
+            rb.rope_attn_cache_attn(*b.head, b.c["q"], ws=small)
+        assert rb.STATUS[e.value.code] == "RA_ERR_WORKSPACE"
+    for got, want in zip(*results):
+        assert torch.equal(got, want) and got.dtype == want.dtype and got.stride() == want.stride()
+
+
 def test_host_tensors_are_refused():
     b = Batch([(1, 40)], 4, 2, 64, 16, "bf16").device()
     for i in range(1, 5):
