@@ -22,11 +22,13 @@ namespace {
 // ------------------------------------------------------------------ fp32, CUDA cores
 // A block of 4 warps takes one row tile (R rows) of an item; in a step of 128 keys each warp
 // takes 32.  Scores: a lane owns a key and reads its whole row of codes (16-byte loads), the
-// queries come as broadcasts from shared memory.  Values: a lane owns D / 32 channels and the
-// warp walks the 32 keys, the weights coming as broadcasts.  Everything is fp32: a code becomes
+// queries come as broadcasts from shared memory.  Values: the two blocks' codes are fetched
+// whole before the scores (16 bytes a lane and load) and go through shared memory; a lane owns
+// D / 32 channels and the warp walks the 32 keys, the weights coming as broadcasts.  Everything is fp32: a code becomes
 // the float 2^23 + code by or-ing it under that exponent, minus 2^23 (both exact), and
 // lo + step * code is rounded once.
 constexpr int kF32Threads = 128;
+constexpr int kF32Blocks = 3 * kSms;  // one wave of the widest tile's registers
 
 template <int D, int R>
 __global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const __grid_constant__ AttnArgs a) {
@@ -34,6 +36,9 @@ __global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const __gri
   __shared__ __align__(16) float q_s[R][D];
   __shared__ __align__(16) float p_s[4][32][R];
   __shared__ float o_s[4][R][D];
+  constexpr int VB = block_bytes(D) / 2;      // codes and pairs of a block's values
+  constexpr int VL = (2 * VB / 16 + 31) / 32; // 16-byte loads of a lane for two blocks
+  __shared__ __align__(16) uint8_t v_s[4][2 * VB];
   __shared__ float ml_s[4][R][2];
   __shared__ long long scratch[8];
   const CacheDims& c = a.c;
@@ -84,6 +89,20 @@ __global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const __gri
       if (key < s.w.L) {
         const int page = page_of(c, a.table, s.b, key / kBlock, a.err, K_CACHE_ATTN_F32);
         if (page >= 0) block = a.cache + block_at(c, page, s.h, (key / kBlock) % c.page_blocks);
+      }
+      const uint8_t* vb[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        vb[k] = reinterpret_cast<const uint8_t*>(__shfl_sync(
+            0xffffffffu, reinterpret_cast<unsigned long long>(block), 16 * k));
+        if (vb[k]) vb[k] += value_offset(D);
+      }
+      uint4 vraw[VL];
+#pragma unroll
+      for (int i = 0; i < VL; ++i) {
+        const int at = (lane + 32 * i) * 16, k = at >= VB;
+        vraw[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (at < 2 * VB && vb[k]) vraw[i] = *reinterpret_cast<const uint4*>(vb[k] + at - k * VB);
       }
       float sc[R];
 #pragma unroll
@@ -145,21 +164,24 @@ __global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const __gri
         }
         p_s[warp][lane][r] = p;
       }
+#pragma unroll
+      for (int i = 0; i < VL; ++i)
+        if ((lane + 32 * i) * 16 < 2 * VB)
+          *reinterpret_cast<uint4*>(&v_s[warp][(lane + 32 * i) * 16]) = vraw[i];
       __syncwarp();
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        const uint8_t* vb = reinterpret_cast<const uint8_t*>(__shfl_sync(
-            0xffffffffu, reinterpret_cast<unsigned long long>(block), half * 16));
-        if (!vb) continue;
-        vb += value_offset(D);
+        // a block that is not there holds zeros; keys behind the last token are left out (their
+        // pairs may be anything)
+        const uint8_t* vc = v_s[warp] + half * VB;
         const int n = min(16, s.w.L - (k0 + half * 16));
-        const __half2* pairs = reinterpret_cast<const __half2*>(vb + code_bytes(D)) +
+        const __half2* pairs = reinterpret_cast<const __half2*>(vc + code_bytes(D)) +
                                (lane * DL) / kGroup;
 #pragma unroll 4
         for (int j = 0; j < n; ++j) {
           uint32_t w;
-          if constexpr (DL == 4) w = reinterpret_cast<const uint16_t*>(vb + j * (D / 2))[lane];
-          else w = vb[j * (D / 2) + lane];
+          if constexpr (DL == 4) w = reinterpret_cast<const uint16_t*>(vc + j * (D / 2))[lane];
+          else w = vc[j * (D / 2) + lane];
           const float2 pr = __half22float2(pairs[j * (D / kGroup)]);
           float v[DL];
 #pragma unroll
@@ -354,7 +376,7 @@ cudaError_t launch_f32(AttnArgs& a, int rows, cudaStream_t s) {
   else if (rows <= 2) a.tile = 2, kernel = cache_attn_f32_kernel<D, 2>;
   else if (rows <= 4) a.tile = 4, kernel = cache_attn_f32_kernel<D, 4>;
   else a.tile = 8, kernel = cache_attn_f32_kernel<D, 8>;
-  return launch_overlapped(kernel, dim3(kRowsBlocks), kF32Threads, 0, s, a);
+  return launch_overlapped(kernel, dim3(kF32Blocks), kF32Threads, 0, s, a);
 }
 
 }  // namespace
@@ -427,7 +449,7 @@ ra_status rope_attn_cache_attn(const ra_cache* p, const void* cache, const int32
     a.min_steps = 1;
     const TimingScope timed(K_CACHE_ATTN_F32, s);
     const int rows = (int)std::min<int64_t>(most_rows, 8);
-    ca.blocks[0] = kRowsBlocks;
+    ca.blocks[0] = kF32Blocks;
     e = p->d == 64 ? launch_f32<64>(a, rows, s) : launch_f32<128>(a, rows, s);
   } else {
     // every sequence goes to the kernel for its own number of rows, whatever the others have

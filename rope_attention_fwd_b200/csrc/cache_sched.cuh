@@ -70,12 +70,33 @@ __device__ inline Run find_run(const AttnArgs& a, long long* scratch, int kid) {
       const int fault = sequence_fault(a.c, a.indptr[b], a.indptr[b + 1], a.kv_len[b]);
       if (fault) record_cache_fault(a.err, kid, fault, b);
     }
+  Run r;
+  if (a.c.B <= 32) {
+    // a warp holds the whole batch: every warp finds the run for itself, nothing is shared
+    mine = lane < a.c.B ? load_work(a, lane).total : 0;
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    total = __shfl_sync(0xffffffffu, x, 31);
+    before = x - mine;
+    r.per = steps_per_block(total, (int)gridDim.x, a.min_steps);
+    r.whole = whole_steps(r.per, a.tile);
+    r.begin = min(total, (long long)blockIdx.x * r.per);
+    r.end = min(total, r.begin + r.per);
+    const unsigned hit = __ballot_sync(
+        0xffffffffu, mine > 0 && r.begin >= before && r.begin < before + mine);
+    r.b = hit ? __ffs(hit) - 1 : 0;
+    r.base = __shfl_sync(0xffffffffu, before, r.b);
+    return r;
+  }
   for (int b0 = 0; b0 < a.c.B; b0 += n) {
     long long chunk;
     chunk_scan(b0, chunk);
     total += chunk;
   }
-  Run r;
   r.per = steps_per_block(total, (int)gridDim.x, a.min_steps);
   r.whole = whole_steps(r.per, a.tile);
   r.begin = min(total, (long long)blockIdx.x * r.per);
