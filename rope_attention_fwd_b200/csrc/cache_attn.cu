@@ -24,14 +24,22 @@ namespace {
 // takes 32.  Scores: a lane owns a key and reads its whole row of codes (16-byte loads), the
 // queries come as broadcasts from shared memory.  Values: the two blocks' codes are fetched
 // whole before the scores (16 bytes a lane and load) and go through shared memory; a lane owns
-// D / 32 channels and the warp walks the 32 keys, the weights coming as broadcasts.  Everything is fp32: a code becomes
-// the float 2^23 + code by or-ing it under that exponent, minus 2^23 (both exact), and
-// lo + step * code is rounded once.
+// D / 32 channels and the warp walks the 32 keys, the weights coming as broadcasts.  Everything
+// is fp32: a code becomes the float 2^23 + code by or-ing it under that exponent, minus 2^23
+// (both exact), and lo + step * code is rounded once.  What bounds it is the CUDA cores' issue
+// (2 d multiplications and as many conversions a row and key against half a byte of cache):
+// 2 prompt chunks of 100 to 200 tokens, 32 / 8 heads, d 128, to 1000 keys: 298 us, 17.6 TFLOP/s;
+// 6 sequences of 2 to 4 tokens, 8 / 2 heads, d 64, to 4099 keys: 22 us, of which the block's cut
+// of the work is 3 and the join 2.5.
 constexpr int kF32Threads = 128;
-constexpr int kF32Blocks = 3 * kSms;  // one wave of the widest tile's registers
+// Blocks of an SM: one wave of as many as the tile's registers let in.  One row, 8 caches to 8000
+// tokens, d 128: 32 us with 4, 40 with 3; 8 rows: 47 with 3 (100 bytes spilled), 68 with 2.
+constexpr int f32_ctas(int R) { return R <= 2 ? 4 : 3; }
+static_assert(f32_ctas(1) * kSms <= kRowsBlocks, "the workspace holds kRowsBlocks parts");
 
 template <int D, int R>
-__global__ void __launch_bounds__(kF32Threads) cache_attn_f32_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kF32Threads, f32_ctas(R))
+    cache_attn_f32_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int DL = D / 32;  // channels of a lane in the value product
   __shared__ __align__(16) float q_s[R][D];
   __shared__ __align__(16) float p_s[4][32][R];
@@ -369,19 +377,16 @@ __global__ void __launch_bounds__(kCombineThreads)
 }
 
 template <int D>
-cudaError_t launch_f32(AttnArgs& a, int rows, cudaStream_t s) {
+cudaError_t launch_f32(AttnArgs& a, int64_t rows, int* blocks, cudaStream_t s) {
   // the smallest tile that holds the rows of the longest sequence
   void (*kernel)(AttnArgs);
   if (rows <= 1) a.tile = 1, kernel = cache_attn_f32_kernel<D, 1>;
   else if (rows <= 2) a.tile = 2, kernel = cache_attn_f32_kernel<D, 2>;
   else if (rows <= 4) a.tile = 4, kernel = cache_attn_f32_kernel<D, 4>;
   else a.tile = 8, kernel = cache_attn_f32_kernel<D, 8>;
-  return launch_overlapped(kernel, dim3(kF32Blocks), kF32Threads, 0, s, a);
+  *blocks = f32_ctas(a.tile) * kSms;
+  return launch_overlapped(kernel, dim3(*blocks), kF32Threads, 0, s, a);
 }
-
-}  // namespace
-
-namespace {
 
 // rows: most rows of an item.
 cudaError_t launch_combine(const CombineArgs& ca, int32_t dtype, int d, int rows,
@@ -448,9 +453,8 @@ ra_status rope_attn_cache_attn(const ra_cache* p, const void* cache, const int32
   if (p->dtype == RA_F32) {
     a.min_steps = 1;
     const TimingScope timed(K_CACHE_ATTN_F32, s);
-    const int rows = (int)std::min<int64_t>(most_rows, 8);
-    ca.blocks[0] = kF32Blocks;
-    e = p->d == 64 ? launch_f32<64>(a, rows, s) : launch_f32<128>(a, rows, s);
+    e = p->d == 64 ? launch_f32<64>(a, most_rows, &ca.blocks[0], s)
+                   : launch_f32<128>(a, most_rows, &ca.blocks[0], s);
   } else {
     // every sequence goes to the kernel for its own number of rows, whatever the others have
     a.max_rows = kChunkMinRows;
