@@ -9,18 +9,20 @@
 //     blocks into a private ring of shared memory (one cp.async.bulk per block, its own
 //     mbarriers) and keeps its own online softmax.  The four warps of a block meet only at the
 //     end of an item.
-//   * A code never becomes its value.  Or-ing four bits into the mantissa of an fp16 constant
-//     gives 1024 + c (bits 0-3) or 64 + c (bits 4-7), a packed subtraction c - 8, exactly: a
-//     word of eight codes is four operand registers for one shift, four logic operations and
-//     four subtractions.  (Leaving the bias in and taking it off the sums saves the
-//     subtractions, but the tensor cores' fp32 sums do not round to nearest: of 32768 nearly
-//     equal weights the output was 1.4% off, and the log-sum-exp 6e-6.)  What the (step, lo)
-//     pairs add is linear and comes in outside the inner products, with mid = lo + 8 step:
+//   * A code never becomes its value.  Four bits alone are an fp16 number already, the subnormal
+//     c 2^-24 (bits 0-3) or c 2^-20 (bits 4-7), which the tensor cores multiply exactly: a word
+//     of eight codes is four operand registers for one shift and four masks.  The two powers of
+//     two are taken out of the sums, which are kept apart for even and odd channels.  What the
+//     (step, lo) pairs add is linear and comes in outside the inner products:
 //   * S^T = K Q^T with mma.sync.m16n8k16: 16 keys are the M rows, the (up to 8 per tile) query
-//     rows the N columns; then s = step (q . (c - 8)) + mid sum(q), per key and group.
+//     rows the N columns; then s = step (q . c) + lo sum(q), per key and group.
 //   * P V as O^T = V^T P^T: channels are the M rows, P^T the B operand, scaled by the keys' steps
 //     before it is rounded to fp16 (one copy per group of 64 channels) and turned around in
-//     registers by movmatrix; sum(p mid) is kept in fp32.
+//     registers by movmatrix; sum(p mid) with mid = lo + 8 step is kept in fp32.
+//   * The sums over keys have to stay near zero mean: the tensor cores' fp32 sums do not round to
+//     nearest, and with codes moved by 1024 the output of 32768 nearly equal weights was 1.4%
+//     off.  So -8 sum(p step), of the rounded operands, is made by one product with a constant
+//     matrix per group and added to the group's accumulators every kFold shares.
 //   * Which key or channel sits in which MMA row is free as long as both products agree; it is
 //     chosen so that every shared-memory read is a conflict-free or two-way 4- or 8-byte
 //     access of the cache's plain channel order.
@@ -47,10 +49,12 @@ namespace {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStages = 3;             // ring of a warp, in its 32-token shares of a step
 constexpr float kTau = 2.0f;           // lazy rescale of the running max, log2 units
-constexpr float kMid = 8.f;            // codes enter the products as c - kMid
-// fp16 pairs: 1024 and 64 (a code or-ed into their mantissas adds itself), and those + kMid
-constexpr uint32_t kEvenBits = 0x64006400u, kOddBits = 0x54005400u;
-constexpr uint32_t kEvenMid = 0x64086408u, kOddMid = 0x54805480u;
+constexpr int kFold = 4;               // shares between two moves of the sums by -kMid
+constexpr float kMid = 8.f;
+// pairs of codes as fp16 subnormals: c 2^-24 in bits 0-3, c 2^-20 in bits 4-7; and -kMid alike
+constexpr uint32_t kEven = 0x000f000fu, kOdd = 0x00f000f0u;
+constexpr uint32_t kEvenMid = 0x80088008u, kOddMid = 0x80808080u;
+constexpr float kEvenUnit = 16777216.f, kOddUnit = 1048576.f;  // 2^24, 2^20
 
 template <int D, int NT>
 struct RowsCfg {
@@ -67,26 +71,22 @@ struct RowsCfg {
   static constexpr int SMEM = OFF_WALK + (int)sizeof(SharedWalk);
 };
 
+// d = A B, plus d itself unless First
+template <bool First = false>
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
-                                        float c2, float c3) {
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(First ? 0.f : d[0]),
+        "f"(First ? 0.f : d[1]), "f"(First ? 0.f : d[2]), "f"(First ? 0.f : d[3]));
 }
 // The 8 x 8 matrix of 16-bit elements held by the warp (lane: row lane / 4, columns
 // 2 (lane % 4), + 1) transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-// (x & mask) | bits in one logic operation.
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
-  uint32_t y;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
   return y;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
@@ -101,14 +101,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
 }
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
-
-// The A registers of two channels, c - 8 each, from the low eight bits of each half of x.
-__device__ __forceinline__ uint32_t even_codes(uint32_t x) {
-  return as_u32(__hsub2(as_half2(and_or(x, 0x000f000fu, kEvenBits)), as_half2(kEvenMid)));
-}
-__device__ __forceinline__ uint32_t odd_codes(uint32_t x) {
-  return as_u32(__hsub2(as_half2(and_or(x, 0x00f000f0u, kOddBits)), as_half2(kOddMid)));
-}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
@@ -126,7 +118,8 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
   float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE);
   float* ml_s = reinterpret_cast<float*>(smem + C::OFF_ML);
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * kStages;
-  const float scale_log2 = c.scale * 1.4426950408889634f;
+  // scores are kept in units of 2^-20, as the codes' products come
+  const float scale_log2 = c.scale * 1.4426950408889634f * kOddUnit;
 
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&bar[i], 1);
@@ -261,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum *= 1.f / kOddUnit;
         qs[nt][g] = make_float2(__shfl_sync(0xffffffffu, sum, 8 * t),
                                 __shfl_sync(0xffffffffu, sum, 8 * t + 4));
       }
@@ -270,17 +264,34 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
     // running maximum (log2 units), sums of p, O without and sums of p mid
     float m2[NT][2], o[NT][MT][4];
     float2 l[NT], pmid[NT][NG];
+    float shift[NT][NG][4];  // -kMid times the sums of p step since the last fold
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m2[nt][0] = m2[nt][1] = -CUDART_INF_F;
       l[nt] = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int g = 0; g < NG; ++g) pmid[nt][g] = make_float2(0.f, 0.f);
+      for (int g = 0; g < NG; ++g) {
+        pmid[nt][g] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) shift[nt][g][e] = 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
     }
+    auto fold = [&] {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+#pragma unroll
+            for (int i2 = 0; i2 < 4; ++i2) o[nt][4 * g + i2][e] += shift[nt][g][e];
+            shift[nt][g][e] = 0.f;
+          }
+    };
     for (int i = i0; i < i1; ++i) {
       if (gave_up) break;
       const int stage = consumed % kStages;
@@ -303,34 +314,31 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
         for (int g = 0; g < NG; ++g) {
           const uint2 wa = lds64(kb + krow * (D / 2) + g * 32 + t * 8);
           const uint2 wb = lds64(kb + (krow + 8) * (D / 2) + g * 32 + t * 8);
-          float2 pa = __half22float2(as_half2(lds32(pairs + (krow * NG + g) * 4)));
-          float2 pb = __half22float2(as_half2(lds32(pairs + ((krow + 8) * NG + g) * 4)));
-          pa.y = fmaf(kMid, pa.x, pa.y);
-          pb.y = fmaf(kMid, pb.x, pb.y);
-          float acc[NT][4];
+          const float2 pa = __half22float2(as_half2(lds32(pairs + (krow * NG + g) * 4)));
+          const float2 pb = __half22float2(as_half2(lds32(pairs + ((krow + 8) * NG + g) * 4)));
+          const uint32_t xa = wa.x >> 8, xb = wb.x >> 8, ya = wa.y >> 8, yb = wb.y >> 8;
+          float even[NT][4], odd[NT][4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t xa = j < 2 ? wa.x : wa.y, xb = j < 2 ? wb.x : wb.y;
-            if (j % 2) xa >>= 8, xb >>= 8;
-            const uint32_t a0 = even_codes(xa), a1 = even_codes(xb);
-            const uint32_t a2 = odd_codes(xa), a3 = odd_codes(xb);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (j == 0)
-                mma_f16(acc[nt], a0, a1, a2, a3, qb[nt][g][0], qb[nt][g][1], 0.f, 0.f, 0.f, 0.f);
-              else
-                mma_f16(acc[nt], a0, a1, a2, a3, qb[nt][g][2 * j], qb[nt][g][2 * j + 1],
-                        acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
-            }
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t (&q)[8] = qb[nt][g];
+            mma_f16<true>(even[nt], wa.x & kEven, wb.x & kEven, xa & kEven, xb & kEven, q[0], q[2]);
+            mma_f16<true>(odd[nt], wa.x & kOdd, wb.x & kOdd, xa & kOdd, xb & kOdd, q[1], q[3]);
+            mma_f16(even[nt], wa.y & kEven, wb.y & kEven, ya & kEven, yb & kEven, q[4], q[6]);
+            mma_f16(odd[nt], wa.y & kOdd, wb.y & kOdd, ya & kOdd, yb & kOdd, q[5], q[7]);
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
+            const float2 sixteen = make_float2(16.f, 16.f);  // units of 2^-24 to 2^-20
+            const float2 ua = ffma2(make_float2(even[nt][0], even[nt][1]), sixteen,
+                                    make_float2(odd[nt][0], odd[nt][1]));
+            const float2 ub = ffma2(make_float2(even[nt][2], even[nt][3]), sixteen,
+                                    make_float2(odd[nt][2], odd[nt][3]));
             // scalar FMAs: the packed form would first have to double step and lo
             float2 &x = sc[k][nt][0], &y = sc[k][nt][1];
-            x.x = fmaf(pa.x, acc[nt][0], g ? fmaf(pa.y, qs[nt][g].x, x.x) : pa.y * qs[nt][g].x);
-            x.y = fmaf(pa.x, acc[nt][1], g ? fmaf(pa.y, qs[nt][g].y, x.y) : pa.y * qs[nt][g].y);
-            y.x = fmaf(pb.x, acc[nt][2], g ? fmaf(pb.y, qs[nt][g].x, y.x) : pb.y * qs[nt][g].x);
-            y.y = fmaf(pb.x, acc[nt][3], g ? fmaf(pb.y, qs[nt][g].y, y.y) : pb.y * qs[nt][g].y);
+            x.x = fmaf(pa.x, ua.x, g ? fmaf(pa.y, qs[nt][g].x, x.x) : pa.y * qs[nt][g].x);
+            x.y = fmaf(pa.x, ua.y, g ? fmaf(pa.y, qs[nt][g].y, x.y) : pa.y * qs[nt][g].y);
+            y.x = fmaf(pb.x, ub.x, g ? fmaf(pb.y, qs[nt][g].x, y.x) : pb.y * qs[nt][g].x);
+            y.y = fmaf(pb.x, ub.y, g ? fmaf(pb.y, qs[nt][g].y, y.y) : pb.y * qs[nt][g].y);
           }
         }
       }
@@ -384,7 +392,11 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
           }
           l[nt] = fmul2(l[nt], corr);
 #pragma unroll
-          for (int g = 0; g < NG; ++g) pmid[nt][g] = fmul2(pmid[nt][g], corr);
+          for (int g = 0; g < NG; ++g) {
+            pmid[nt][g] = fmul2(pmid[nt][g], corr);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) shift[nt][g][e] *= e % 2 ? corr.y : corr.x;
+          }
 #pragma unroll
           for (int i2 = 0; i2 < MT; ++i2)
 #pragma unroll
@@ -453,16 +465,22 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 float (&x)[4] = o[nt][4 * g + 2 * hl + i2];
-                mma_f16(x, even_codes(x01), odd_codes(x01), even_codes(x23), odd_codes(x23),
-                        pb[nt][g][0], pb[nt][g][1], x[0], x[1], x[2], x[3]);
+                mma_f16(x, x01 & kEven, x01 & kOdd, x23 & kEven, x23 & kOdd, pb[nt][g][0],
+                        pb[nt][g][1]);
               }
             }
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16(shift[nt][g], kEvenMid, kOddMid, kEvenMid, kOddMid, pb[nt][g][0],
+                    pb[nt][g][1]);
         }
       }
       __syncwarp();  // every lane has read the stage
       if (next < i1) issue(s, next++);
+      if ((i - i0) % kFold == kFold - 1) fold();
     }
+    fold();
 
     // ---- sum(p mid) in: a group's channels all get the same
 #pragma unroll
@@ -477,7 +495,9 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D, NT>::CTAS)
 #pragma unroll
         for (int i2 = 0; i2 < 4; ++i2)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[nt][4 * g + i2][e] += e % 2 ? x.y : x.x;
+          for (int e = 0; e < 4; ++e)
+            o[nt][4 * g + i2][e] = fmaf(o[nt][4 * g + i2][e], e < 2 ? kEvenUnit : kOddUnit,
+                                        e % 2 ? x.y : x.x);
       }
     // ---- the four warps' partial softmaxes joined, in the accumulators' own layout
 #pragma unroll

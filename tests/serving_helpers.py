@@ -89,15 +89,20 @@ class Batch:
         """Every row against the float64 oracle.  Tolerance of an element, U = 2^-24:
           stored type: half a step of |o|;
           a score: fp32 products and sums over d channels and the two affine terms of each
-            group, at most (d + 16) U scale sum |q| (|k| + the 8 steps that the codes are moved by) =: ds, which moves p by 2 ds relative (numerator and sum);
+            group, at most (d + 16) U scale sum |q| (|k| + the 8 steps that the codes may be moved
+            by) =: ds, which moves p by 2 ds relative (numerator and sum).  (Where the codes
+            enter as 0..15, the terms are 15 steps + |lo|, at most 3 |k|, with some 16
+            roundings: (d + 16) 2.07 is more than 16 x 3.);
           exp2 and the sums of p: 2^-20 relative (2 ulp of ex2.approx, rescales, sums of at
             most 2^11 terms per lane and step in fp32);
           bf16, more than 64 rows per kv head: p and v are rounded to fp16 (2^-11 each; below 2^-14
             by at most 2^-25 absolute);
           bf16, up to 64 rows: p step is rounded to fp16 (2^-11 relative, 2^-25 below 2^-14) and
-            multiplies codes of -8..7: 8 step (2^-11 + L 2^-25 / step) at most, with
-            step <= 2 vmax / 15; the fp32 sums of the products may lose 2^-23 of themselves with
-            each 16 keys, 8 step at most: L / 16 2^-23 8 step.
+            multiplies codes of -8..7 (0..15, and -8 by the same operand): 8 step (2^-11 +
+            L 2^-25 / step) at most, with step <= 2 vmax / 15; the fp32 sums of the products may
+            lose 2^-23 of themselves with each 16 keys of a warp.  A warp has every fourth 32
+            keys; its sums hold 8 step of all its keys, and 15 step and -8 step of the last 128:
+            (L / 64 + 2) 2^-23 (8 + 15 + 8) step, below L / 16 2^-23 8 step + 2^-17 step.
         All of it relative to sum_j p_j |v_j|; lse moves by ds + 2^-20 and its own rounding."""
         U, bf = 2.0 ** -24, self.dtype == torch.bfloat16
         q = self.q.double().numpy() if q is None else q
@@ -119,7 +124,8 @@ class Batch:
                 tol = tol + 2 * 2.0 ** -11 * mag * 1.01 + L * 2.0 ** -25 * vmax + 2.0 ** -25
             elif bf:
                 step = 2 * vmax / 15 * 1.01
-                tol = tol + 8 * step * (2.0 ** -11 + L / 16 * 2.0 ** -23) + 8 * L * 2.0 ** -25
+                tol = tol + 8 * step * (2.0 ** -11 + L / 16 * 2.0 ** -23 + 2.0 ** -20)
+                tol = tol + 8 * L * 2.0 ** -25
             err = abs(o[at] - wo)
             assert np.isfinite(o[at]).all(), (label, b)
             assert (err <= tol).all(), (label, b, float((err / tol).max()))
