@@ -295,8 +295,8 @@ ra_status rope_attn_rotary_bwd(const ra_rotary* r, int64_t B, int64_t n, int32_t
  * the sequence's own tokens), or a used page outside 0..pages-1 is recorded as RA_ERR_CACHE
  * (info: kernel id, what (RA_CACHE_BAD_*), sequence) and never followed: a bad sequence is
  * skipped (its outputs are not valid), the tokens of a bad page are neither written nor read
- * (attention sees them as masked, reads give zeros).  Sequences may share pages to read; two sequences that append to one slot in
- * one call leave it undefined.
+ * (attention sees them as masked, reads give zeros).  Sequences may share pages to read; two
+ * sequences that append to one slot in one call leave it undefined.
  *
  * ws (all calls): rope_attn_cache_workspace_bytes(p) bytes, 256-byte aligned.  Its first 64
  * bytes are the error word: zero them once; the calls never clear it (the first error stays
@@ -352,7 +352,8 @@ ra_status rope_attn_cache_read(const ra_cache* p, const void* cache, const int32
  *   bf16, more: tcgen05; K as exact fp16 products (step (code - 8) rounded to fp16 where a row
  *     sees 4096 keys or more), V rounded to fp16, weights fp16.
  *   In both q enters as fp16: entries, and in the second kernel sums of 64 channels, beyond
- *     65504 are clamped and reported as RA_ERR_RANGE.
+ *     65504 are clamped and reported as RA_ERR_RANGE; entries below 2^-14 are rounded to
+ *     multiples of 2^-24.
  *   fp32: CUDA cores, fp32 throughout. */
 ra_status rope_attn_cache_attn(const ra_cache* p, const void* cache, const int32_t* table,
                                const int32_t* indptr, const int32_t* kv_len, const ra_rows* q,

@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(R))
 // Block x joins the split item that begins in block x of an attention launch (of the first
 // launch's blocks, then of the second's).  Few parts: a warp takes a row, blockIdx.y and the
 // block's warps share the rows.  Many parts (one long cache over most of the GPU, few rows): the
-// block takes a row, its warps share the parts.
+// block takes a row, its warps share the parts.  Bound by latency: it adds 2.5 us to a call whose
+// items are split, one launch for both attention kernels' parts.
 constexpr int kCombineThreads = 256, kCombineWarps = kCombineThreads / 32;
 constexpr int kWarpParts = 16;  // most parts that one warp walks alone
 

@@ -34,8 +34,16 @@
 // row sees few keys (1e-5 of it; over 4096 keys of like weight 3e-7).  So where the tile's first
 // row sees fewer than kExactKeys keys the step is cut into its upper eight and lower three bits,
 // s1 + s2: s (code - 8) then has at most 11 bits, and K is two exact operand tiles instead of
-// one.  Exact products take a fifth more time (2048 tokens over 8192, 32 heads of 128 on 8:
-// 650 us against 541): operands from shared memory saturate its bandwidth.
+// one.  Exact products take a fifth more time: operands from shared memory saturate its
+// bandwidth (two chunks of 900 to 2048 tokens over 3000 to 8192, 32 heads of 128 on 8: 650 us
+// with all of them exact, 541 with none, 560 by this rule).
+//
+// What bounds it.  At those sizes 560 us = 836 TFLOP/s, half of what dense library products
+// reach: the tensor pipe is busy 43% of the cycles and the exponentials' 42%, since a row tile's
+// chain (scores, softmax, values) is walked one step at a time and two tiles are all that TMEM
+// holds.  More unpacking or softmax warps (20 and 28 in all), other register splits and a P
+// handed over in halves were each slower; all that it reads and writes (75 MB) is
+// 2% of the time.
 //
 // Numerics otherwise: q as fp16 (converted from bf16, clamped and reported as RA_ERR_RANGE
 // beyond 65504, the sums of 64 channels too), v = lo + step code rounded once to fp16, P as fp16,

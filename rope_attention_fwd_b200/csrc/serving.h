@@ -66,12 +66,11 @@ __host__ __device__ inline int sequence_fault(const CacheDims& c, int q0, int q1
 constexpr int kStep = 128;
 constexpr int kSms = 148;
 // What an item of few rows costs besides its keys (queries in, partial results joined, results
-// out), in steps: empty steps at its end that weigh in the cut and are never walked.  Measured:
-// 4 us an item against 1.7 us a step; without them the blocks that draw many short items finish
-// last (16 caches of 100 to 32768 tokens, 8 kv heads: 83 us for the slowest block against 61 in
-// the middle, 70 against 61 with them).  Items of the chunk kernel cost less than one of its
-// steps (and rising ones have an empty step already): 562 us with, 535 without at 2048 tokens
-// over 8192.
+// out), in steps: empty steps at its end that weigh in the cut and are never walked.  An item
+// costs about 2.4 of its steps; without them the blocks that draw many short items finish last
+// (16 caches of 100 to 32768 tokens, 8 kv heads: 83 us for the slowest block against 61 in the
+// middle, 70 against 61 with them).  Items of the chunk kernel cost less than one of its steps
+// (and rising ones have an empty step already): 5% slower with them.
 constexpr int kItemSteps = 2;
 constexpr int kRowsTile = 16;      // most rows of a tile of the kernels for few rows
 
