@@ -254,7 +254,8 @@ ra_status rope_attn_rotary_freqs(const ra_rotary* r, const float* alpha, double*
  * (any sign), or NULL for i at token i.  k and k_out may both be NULL.  An output may be its
  * input (same pointer and strides), not overlap it otherwise.  The angle is formed and reduced
  * in fp64, cos and sin rounded to fp32, the turn computed in fp32 and rounded once to the
- * dtype.  B n <= 2^30. */
+ * dtype.  Angles |p theta_hat| beyond 2^50, where fp64 no longer resolves a turn, give no valid
+ * result.  B, n >= 1, B n <= 2^30. */
 ra_status rope_attn_rotary(const ra_rotary* r, int64_t B, int64_t n, int32_t dtype,
                            const double* freqs, const int32_t* pos, const ra_rows* q,
                            const ra_rows* q_out, const ra_rows* k, const ra_rows* k_out,
@@ -341,8 +342,8 @@ ra_status rope_attn_cache_read(const ra_cache* p, const void* cache, const int32
                                const ra_rows* v, void* ws, size_t ws_bytes, void* stream);
 
 /* o = softmax(scale q K^T + mask) V over the cache, lse = log-sum-exp of each row (natural
- * log).  q [T, Hq, d] rows (already rotated), o dense [T, Hq, d] (16-byte aligned), lse dense
- * fp32 [T, Hq]; q head h reads kv head h / (Hq / Hkv).  A row that sees no key gives o = 0,
+ * log).  q [T, Hq, d] rows (already rotated), o dense [T, Hq, d] (16-byte aligned; it may be a
+ * dense q, but not overlap it otherwise), lse dense fp32 [T, Hq]; q head h reads kv head h / (Hq / Hkv).  A row that sees no key gives o = 0,
  * lse = -inf.  The pairs of cached tokens must be finite, as appending writes them (what lies
  * behind kv_len may be anything).  Deterministic: no atomics, fixed order; a sequence's result
  * does not depend on the others' contents, only (by rounding) on how the lengths cut the work.

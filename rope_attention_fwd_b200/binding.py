@@ -396,7 +396,14 @@ def _load_marshal():
 
 
 _fast = _load_marshal()
-_address = ctypes.addressof
+
+
+def _address(s, kind):
+    """The address of a spec or plan for _marshal, which takes it on trust."""
+    if s.__class__ is not kind:
+        raise TypeError(f"expected {kind.__name__}, got {type(s).__name__}")
+    return ctypes.addressof(s)
+
 
 
 def _done(fn, out):
@@ -479,7 +486,7 @@ def rope_attn_rotary_freqs(spec, alpha=None, freqs=None, device=None):
     computed anew whenever alpha changes."""
     fn = "rope_attn_rotary_freqs"
     if _fast is not None and freqs is None and alpha is not None:
-        out = _fast.rotary_freqs(_address(spec), alpha)
+        out = _fast.rotary_freqs(_address(spec, RaRotary), alpha)
         if out is not None:
             return _done(fn, out)
     half = spec.rot_dim // 2
@@ -519,7 +526,7 @@ def rope_attn_rotary(spec, freqs, q, k=None, pos=None, q_out=None, k_out=None):
     None) rotated at positions pos (int32 [B, n]; None: 0..n-1).  q_out may be q, k_out k."""
     fn = "rope_attn_rotary"
     if _fast is not None and q_out is None and k_out is None:
-        out = _fast.rotary(_address(spec), freqs, q, k, pos)
+        out = _fast.rotary(_address(spec, RaRotary), freqs, q, k, pos)
         if out is not None:
             return _done(fn, out)
     dev, head = _rotary_args(fn, spec, freqs, q, pos)
@@ -548,7 +555,7 @@ def rope_attn_rotary_bwd(spec, freqs, dq_rot, dk_rot=None, q=None, k=None, pos=N
     fn = "rope_attn_rotary_bwd"
     if _fast is not None and not frozen_alpha and dq is None and dk is None and dalpha is None \
             and ws is None:
-        out = _fast.rotary_bwd(_address(spec), freqs, dq_rot, dk_rot, q, k, pos)
+        out = _fast.rotary_bwd(_address(spec, RaRotary), freqs, dq_rot, dk_rot, q, k, pos)
         if out is not None:
             return _done(fn, out)
     dev, head = _rotary_args(fn, spec, freqs, dq_rot, pos)
@@ -654,8 +661,8 @@ def rope_attn_cache_append(plan, cache, table, indptr, kv_len, spec, freqs, k, v
     value beyond the cache's range) stay in ws for rope_attn_device_status."""
     fn = "rope_attn_cache_append"
     if _fast is not None and q_out is None:
-        out = _fast.cache_append(_address(plan), cache, table, indptr, kv_len, _address(spec),
-                                 freqs, k, v, q, ws)
+        out = _fast.cache_append(_address(plan, RaCache), cache, table, indptr, kv_len,
+                                 _address(spec, RaRotary), freqs, k, v, q, ws)
         if out is not None:
             return _done(fn, out)[0]
     dev, head, tail, dt = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)
@@ -676,7 +683,7 @@ def rope_attn_cache_read(plan, cache, table, indptr, kv_len, k=None, v=None, ws=
     (for a whole cache, give indptr the running sum of kv_len)."""
     fn = "rope_attn_cache_read"
     if _fast is not None and k is None and v is None:
-        out = _fast.cache_read(_address(plan), cache, table, indptr, kv_len, ws)
+        out = _fast.cache_read(_address(plan, RaCache), cache, table, indptr, kv_len, ws)
         if out is not None:
             return _done(fn, out)
     dev, head, tail, dt = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)
@@ -694,7 +701,7 @@ def rope_attn_cache_attn(plan, cache, table, indptr, kv_len, q, o=None, lse=None
     cache.  Rows that belong to no sequence are left as they were."""
     fn = "rope_attn_cache_attn"
     if _fast is not None and o is None and lse is None:
-        out = _fast.cache_attn(_address(plan), cache, table, indptr, kv_len, q, ws)
+        out = _fast.cache_attn(_address(plan, RaCache), cache, table, indptr, kv_len, q, ws)
         if out is not None:
             return _done(fn, out)
     dev, head, tail, dt = _cache_args(fn, plan, cache, table, indptr, kv_len, ws)

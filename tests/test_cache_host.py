@@ -322,3 +322,17 @@ def test_reference_quantiser_is_within_half_a_step():
         slack = np.abs(lo).astype(float) * 2.0 ** -11 + 15 * step.astype(float) * 2.0 ** -11 + 1e-6
         assert (np.abs(y - x) <= (0.5 * step.astype(float) + slack).repeat(64, -1)).all()
         assert codes.max() == 15 and codes[0].max() == 0
+
+
+@pytest.mark.skipif(rb._fast is None, reason="extension not built")
+def test_a_plan_and_a_spec_are_not_taken_for_each_other():
+    """The extension reads them by address, so the binding looks at what they are."""
+    plan, spec, x = _plan(), rb.rotary_spec(128), torch.zeros(1)
+    for call in (lambda: rb.rope_attn_cache_attn(spec, x, x, x, x, x, ws=x),
+                 lambda: rb.rope_attn_cache_read(spec, x, x, x, x, ws=x),
+                 lambda: rb.rope_attn_cache_append(plan, x, x, x, x, plan, x, x, x, ws=x),
+                 lambda: rb.rope_attn_rotary(plan, x, x),
+                 lambda: rb.rope_attn_rotary_freqs(plan, x),
+                 lambda: rb.rope_attn_rotary_bwd(None, x, x)):
+        with pytest.raises(TypeError):
+            call()

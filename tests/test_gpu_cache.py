@@ -496,3 +496,31 @@ def test_serving_run(dtype, layout):
             t += n
             rows.append(tuple(np.concatenate(kept[s][i::2]).transpose(1, 0, 2) for i in (0, 1)))
         check.check(o, lse, q=q_rot.double().cpu().numpy(), rows=rows, label=str(news))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_output_may_be_the_queries(dtype):
+    """Whole items, split ones and (bf16) prompt chunks, d 64 and 128."""
+    for d in (64, 128):
+        b = Batch([(1, 9000), (3, 200), (1, 1), (70, 900), (2, 0)], 4, 2, d, 32, dtype,
+                  seed=d + 1).device()
+        o, lse = b.attn()
+        q = b.c["q"].clone()
+        got, lse2 = rb.rope_attn_cache_attn(*b.head, q, o=q, ws=b.c["ws"])
+        assert got.data_ptr() == q.data_ptr()
+        assert torch.equal(q, o) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("B", [32, 33, 600])
+def test_many_sequences_of_both_kernels(B):
+    """One batch around a warp's lanes and beyond a block's threads: every third sequence has
+    more than 64 rows per kv head, the others few, some nothing."""
+    g = np.random.default_rng(B)
+    lens = []
+    for i in range(B):
+        n = (3, 1, 2)[i % 3]
+        lens.append((n, int(g.integers(0, 260)) if i % 7 else 0))
+    b = Batch(lens, 32, 1, 64, 16, "bf16", seed=B).device()
+    o, lse = b.attn()
+    assert b.status()[0] == 0
+    b.check(o, lse)
