@@ -3,7 +3,7 @@
 //
 // For prompts the floor is HBM (every element read once, 4.5 bits of a cached one written or
 // read), for single tokens latency.  Appending 3 prompts of 1500 to 4095 tokens, 32 query heads
-// turned beside 8 of keys and values, d 128, takes 41 us = 4.3 TB/s: a block's start (search,
+// turned in the half layout beside 8 of keys and values, d 128, takes 39 us = 4.5 TB/s: a block's start (search,
 // page, fp64 angles) and the quantiser's instructions share the time with the loads (issue 62%);
 // splitting the heads over more blocks repeats the start (57 us for two), the first rows fetched
 // before it gained 1%.  Reading 4 caches of 3000 to 8190 tokens back takes 25 us = 5.1 TB/s,
@@ -221,8 +221,11 @@ __device__ __forceinline__ uint32_t quantise8(float (&x)[8], bool& beyond, __hal
 
 // V: 16-byte accesses fit everywhere and a thread's eight channels are rotated alike: all of
 // them or none, in the half layout all of the same half (partners are then whole vectors).
+// Four rows in flight in 7 blocks an SM (bf16: 72 registers) take 51.5 us for the prompts above
+// with the read back, in 6 54 (interleaved: 46 and 49), in 8 57; two rows in 8 blocks 56, eight in
+// 4 55.  fp32 rows hold twice the registers: 6 blocks.
 template <typename T, int D, bool V, bool HALF>
-__global__ void __launch_bounds__(kThreads, 6)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 6)
     cache_append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int U = D / 8;      // threads of a token
   constexpr int N = V ? 4 : 1;  // rows in flight
