@@ -413,11 +413,7 @@ __global__ void __launch_bounds__(kThreads)
         if (h + e >= last) break;
         const float2 pair = __half22float2(*reinterpret_cast<const __half2*>(&pr[e]));
         float x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)  // step * code is exact in fp32: one rounding, of the sum
-          x[j] = fmaf(pair.x,
-                      __uint_as_float(((w[e] >> (4 * j)) & 15u) | 0x4b000000u) - 8388608.f,
-                      pair.y);
+        codes_to_values(w[e], pair.x, pair.y, x);
         store8(dst + (int64_t)(h - first + e) * p.out_h, p.vec, x);
       }
     }

@@ -1,5 +1,6 @@
 // cache.cuh -- device helpers of the paged-cache kernels.
 #pragma once
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "serving.h"
@@ -23,6 +24,24 @@ __device__ __forceinline__ int page_of(const CacheDims& c, const int* __restrict
   if (page_ok(c, page)) return page;
   record_cache_fault(err, kernel_id, RA_CACHE_BAD_PAGE, b);
   return -1;
+}
+
+// lo + step * code of a word's eight codes, rounded once.  Four bits alone are an fp16 subnormal,
+// c 2^-24 or (bits 4-7) c 2^-20, two of them in a masked word; the powers of two go into the step
+// (all exact).
+__device__ __forceinline__ void codes_to_values(uint32_t w, float step, float lo, float (&x)[8]) {
+  const float even = step * 16777216.f, odd = step * 1048576.f;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const uint32_t e = w & 0x000f000fu, o = w & 0x00f000f0u;
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&e));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&o));
+    x[i] = fmaf(even, a.x, lo);
+    x[i + 1] = fmaf(odd, b.x, lo);
+    x[i + 4] = fmaf(even, a.y, lo);
+    x[i + 5] = fmaf(odd, b.y, lo);
+    w >>= 8;
+  }
 }
 
 }  // namespace ra

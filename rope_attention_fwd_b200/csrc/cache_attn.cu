@@ -129,11 +129,7 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas(R))
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               float k[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                k[j] = fmaf(pr.x,
-                            __uint_as_float(((w[e] >> (4 * j)) & 15u) | 0x4b000000u) - 8388608.f,
-                            pr.y);
+              codes_to_values(w[e], pr.x, pr.y, k);
 #pragma unroll
               for (int r = 0; r < R; ++r) {
                 const float4* qv =
