@@ -6,8 +6,8 @@
 // turned in the half layout beside 8 of keys and values, d 128, takes 39 us = 4.5 TB/s: a block's start (search,
 // page, fp64 angles) and the quantiser's instructions share the time with the loads (issue 62%);
 // splitting the heads over more blocks repeats the start (57 us for two), the first rows fetched
-// before it gained 1%.  Reading 4 caches of 3000 to 8190 tokens back takes 25 us = 5.1 TB/s,
-// near the conversions' issue (62% of the integer pipe).  64 tokens: 7 us, with the read back.
+// before it gained 1%.  Reading 4 caches of 3000 to 8190 tokens back takes 24.4 us = 5.25
+// TB/s; fewer or more rows in flight and blocks an SM are no faster (24.4 to 28).  64 tokens: 7 us, with the read back.
 // A thread owns one token and eight
 // neighbouring channels: eight codes are one 32-bit word of the cache, the 64 channels of a
 // (step, lo) pair are eight neighbouring lanes, so that a group's range costs three shuffles

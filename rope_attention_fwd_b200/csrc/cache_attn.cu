@@ -25,15 +25,16 @@ namespace {
 // queries come as broadcasts from shared memory.  Values: the two blocks' codes are fetched
 // whole before the scores (16 bytes a lane and load) and go through shared memory; a lane owns
 // D / 32 channels and the warp walks the 32 keys, the weights coming as broadcasts.  Everything
-// is fp32: a code becomes the float 2^23 + code by or-ing it under that exponent, minus 2^23
-// (both exact), and lo + step * code is rounded once.  What bounds it is the CUDA cores' issue
+// is fp32: codes become floats exactly (keys through fp16 subnormals, values as 2^23 + code less
+// 2^23), and lo + step * code is rounded once.  What bounds it is the CUDA cores' issue
 // (2 d multiplications and as many conversions a row and key against half a byte of cache):
-// 2 prompt chunks of 100 to 200 tokens, 32 / 8 heads, d 128, to 1000 keys: 298 us, 17.6 TFLOP/s;
+// 2 prompt chunks of 100 to 200 tokens, 32 / 8 heads, d 128, to 1000 keys: 294 us, 17.8 TFLOP/s;
 // 6 sequences of 2 to 4 tokens, 8 / 2 heads, d 64, to 4099 keys: 22 us, of which the block's cut
 // of the work is 3 and the join 2.5.
 constexpr int kF32Threads = 128;
 // Blocks of an SM: one wave of as many as the tile's registers let in.  One row, 8 caches to 8000
-// tokens, d 128: 32 us with 4, 40 with 3; 8 rows: 47 with 3 (100 bytes spilled), 68 with 2.
+// tokens, d 128: 29 us with 4, a quarter more with 3; 8 rows: 47 with 3 (160 bytes spilled), 68
+// with 2.
 constexpr int f32_ctas(int R) { return R <= 2 ? 4 : 3; }
 static_assert(f32_ctas(1) * kSms <= kRowsBlocks, "the workspace holds kRowsBlocks parts");
 
