@@ -3,17 +3,17 @@
 //
 // For prompts the floor is HBM (every element read once, 4.5 bits of a cached one written or
 // read), for single tokens latency.  Appending 3 prompts of 1500 to 4095 tokens, 32 query heads
-// turned in the half layout beside 8 of keys and values, d 128, takes 39 us = 4.5 TB/s: a block's start (search,
-// page, fp64 angles) and the quantiser's instructions share the time with the loads (issue 62%);
-// splitting the heads over more blocks repeats the start (57 us for two), the first rows fetched
-// before it gained 1%.  Reading 4 caches of 3000 to 8190 tokens back takes 24.4 us = 5.25
-// TB/s; fewer or more rows in flight and blocks an SM are no faster (24.4 to 28).  64 tokens: 7 us, with the read back.
-// A thread owns one token and eight
-// neighbouring channels: eight codes are one 32-bit word of the cache, the 64 channels of a
-// (step, lo) pair are eight neighbouring lanes, so that a group's range costs three shuffles
-// and nothing goes through shared memory.  The thread finds its sequence, page and angles once
-// and walks the heads (keys, values and queries numbered through); few tokens spread the heads
-// over more blocks.
+// turned in the half layout beside 8 of keys and values, d 128, takes 39 us = 4.5 TB/s: a
+// block's start (search, page, fp64 angles) and the quantiser's instructions share the time with
+// the loads (issue 62%); splitting the heads over more blocks repeats the start (57 us for two),
+// the first rows fetched before it gained 1%.  Reading 4 caches of 3000 to 8190 tokens back
+// takes 24.4 us = 5.25 TB/s; fewer or more rows in flight and blocks an SM are no faster (24.4
+// to 28).  64 tokens: 7 us, with the read back. A thread owns one token and eight neighbouring
+// channels: eight codes are one 32-bit word of the cache, the 64 channels of a (step, lo) pair
+// are eight neighbouring lanes, so that a group's range costs three shuffles and nothing goes
+// through shared memory.  The thread finds its sequence, page and angles once and walks the
+// heads (keys, values and queries numbered through); few tokens spread the heads over more
+// blocks.
 #include <cuda_fp16.h>
 
 #include <cmath>
