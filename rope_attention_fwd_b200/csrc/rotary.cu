@@ -55,21 +55,25 @@ struct RotArgs {
 // fits (fp32, 3 x 16 heads x 1021 x 96 half layout: 22.5 us with four heads, 14 with two; bf16,
 // 4 x 16 x 2048 x 64: 25.6 us with four heads in 2 blocks an SM, 23.8 with two in 4, and
 // 2 x 32 x 8192 x 128: 111 and 106).
-template <typename T, bool HALF, bool BWD>
-struct RotaryShape {
-  static constexpr int kHeads = BWD ? 2 : kUnroll;
-  static constexpr int kBlocks = !BWD ? 2 : sizeof(T) == 4 ? 3 : HALF ? 2 : 4;
-};
+// Single elements need more of both: 8 x (32 + 1) x 895 x 128 with 50 channels rotated in halves,
+// bf16 backward: 223 us with two heads in 2 blocks, 103 with four in 4 (in 6 224, eight in 4 202:
+// spills).
+__host__ __device__ constexpr int rotary_heads(bool vec, bool bwd) {
+  return vec && bwd ? 2 : kUnroll;
+}
+constexpr int rotary_blocks(size_t elem, bool vec, bool half, bool bwd) {
+  return !vec ? 4 : !bwd ? 2 : elem == 4 ? 3 : half ? 2 : 4;
+}
 
 // V: elements of one access (a 16-byte vector, or 1 where sizes, strides or addresses allow
 // no vector).
 template <typename T, int V, bool HALF, bool BWD>
-__global__ void __launch_bounds__(kThreads, (RotaryShape<T, HALF, BWD>::kBlocks))
+__global__ void __launch_bounds__(kThreads, rotary_blocks(sizeof(T), V > 1, HALF, BWD))
     rotary_kernel(const __grid_constant__ RotArgs a) {
   constexpr int W = HALF ? V : (V > 1 ? V : 2);      // channels of the first (or only) piece
   constexpr int NP = HALF ? V : W / 2;               // pairs of a unit
   constexpr int NV = HALF || V == 1 ? 2 : 1;         // accesses of a unit
-  constexpr int N = RotaryShape<T, HALF, BWD>::kHeads;
+  constexpr int N = rotary_heads(V > 1, BWD);
   extern __shared__ double red[];
   const int tt = threadIdx.x / a.units, u = threadIdx.x - tt * a.units;
   const bool rot = u < a.rot_units;
@@ -312,9 +316,11 @@ ra_status run(const ra_rotary* r, int64_t B, int64_t n, int32_t dtype, const dou
   const long long tiles = (a.tokens + a.tile - 1) / a.tile;
   // Few tokens: the heads are split over the blocks' second dimension, at least kUnroll heads
   // each, until there are about eight blocks per SM (the angles are then formed once per
-  // chunk, which idle SMs do for nothing).  With partial torques there are at most kRotaryParts
-  // blocks: chunks as far as that leaves one tile per block, else equal numbers of tiles.
-  const long long want = part ? std::max<long long>(1, kRotaryParts / tiles)
+  // chunk, which idle SMs do for nothing).  With partial torques there is one wave of blocks (7 x
+  // 20 heads x 2221 x 96 in halves: 59 us, 69 with 1.1 waves): chunks as far as that leaves one
+  // tile per block, else equal numbers of tiles; at most kRotaryParts either way.
+  const long long wave = std::min(kRotaryParts, kSms * rotary_blocks(elem, vec, half, bwd));
+  const long long want = part ? std::max<long long>(1, wave / tiles)
                               : (kRotaryBlocks + tiles - 1) / tiles;
   const int64_t chunks = std::max<int64_t>(
       1, std::min<int64_t>(want, (heads + kUnroll - 1) / kUnroll));
@@ -322,7 +328,7 @@ ra_status run(const ra_rotary* r, int64_t B, int64_t n, int32_t dtype, const dou
   const unsigned gy = (unsigned)((heads + a.heads_per_chunk - 1) / a.heads_per_chunk);
   long long gx = tiles;
   if (part) {
-    const long long rounds = (tiles * gy + kRotaryParts - 1) / kRotaryParts;
+    const long long rounds = (tiles * gy + wave - 1) / wave;
     gx = (tiles + rounds - 1) / rounds;
   }
   if (gx > 0x7fffffff) return RA_ERR_UNSUPPORTED;
